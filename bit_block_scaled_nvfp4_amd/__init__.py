@@ -545,3 +545,11 @@ def nvfp4_kv_fp8_load(cache, scale, slot_mapping=None, out_dtype=None, width=Non
                                  _ptr(slot_mapping), tokens, _ptr(out), _dtype_code(out.dtype),
                                  out.stride(0), _stream(cache.device)))
     return out
+
+
+# last: the module builds on the names above
+from .attention import (  # noqa: E402,F401
+    nvfp4_kv_block_tables,
+    nvfp4_kv_fp8_attention,
+    nvfp4_kv_fp8_tree_attention,
+)

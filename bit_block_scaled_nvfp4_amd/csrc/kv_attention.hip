@@ -1,0 +1,542 @@
+// Attention of few query rows over the paged FP8 cache: decode steps, drafted trees, short chunks.
+// Also the kernel that joins partial results, and the rule that divides a call's work.
+//
+// What bounds it: every key and value code is read once per (request, KV head) and used by 16, 32 or
+// 64 rows, so the call is bound by HBM reads.  The kernel therefore keeps as many loads in flight as
+// its registers hold and touches LDS only to join its wavefronts at the end of an item.  A wavefront
+// takes 32 positions at a time, from the cache straight into MFMA operand registers:
+//
+//   scores   S^T[key][row] = K Q^T, v_mfma_f32_16x16x32 with the keys as rows of A.  Lane l holds
+//            key l % 16; the dims of a 32-deep step are permuted (the same way in Q) so that the four
+//            lanes of a key load 64 contiguous bytes at a time.
+//   softmax  a column of S^T is a query row, so a lane's statistics are scalars; lanes l, l ^ 16,
+//            l ^ 32, l ^ 48 share the row.
+//   output   O^T[dim][row] += V^T P^T.  P^T leaves the first product in the operand layout of the
+//            second (its 8 keys of a lane are {4 g .. 4 g + 3} and {16 + 4 g ..}, g = l / 16), so V^T
+//            is loaded in that key order: 8 rows of the cache, head_dim / 16 contiguous bytes each,
+//            16 lanes covering a row; 4 x 4 byte transposes put a dim's keys side by side.
+//
+// The next 32 positions are loaded while the present ones are multiplied; their slots are looked up
+// another step ahead, so the chain block table -> address -> row is never waited for.
+#include "kv_attention_common.h"
+
+namespace nvfp4 {
+namespace {
+
+using namespace attn;
+
+constexpr int kThreads = 256;
+constexpr int kWaves = 4;
+constexpr int kStep = 32;              // positions of a wavefront's step
+constexpr int kUnit = kWaves * kStep;  // positions of a workgroup's step
+
+// Codes of 32 positions as a lane holds them.
+template <int D>
+struct Codes {
+  u32x4 k[2][D / 64];        // keys l % 16 and 16 + l % 16
+  uint32_t v[8][D / 64];     // keys 4 g + i and 16 + 4 g + i
+};
+
+template <int D>
+__device__ __forceinline__ void load_codes(const AttnArgs& a, int32_t slot, const uint8_t* kbase,
+                                           const uint8_t* vbase, int lane, Codes<D>& c) {
+  // a position that is not in the cache reads slot 0 (there is one) and is masked afterwards
+  const int32_t s = slot < 0 ? 0 : slot;
+  const int g = lane >> 4, d16 = lane & 15;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int32_t sk = __shfl(s, 16 * t + d16);
+    const uint8_t* p = kbase + (int64_t)sk * a.cache_ld + g * 16;
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) c.k[t][j] = *reinterpret_cast<const u32x4*>(p + 64 * j);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int32_t sv = __shfl(s, 16 * (e >> 2) + 4 * g + (e & 3));
+    const uint8_t* p = vbase + (int64_t)sv * a.cache_ld + d16 * (D / 16);
+    if constexpr (D == 256) {
+      const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+      c.v[e][0] = w.x; c.v[e][1] = w.y; c.v[e][2] = w.z; c.v[e][3] = w.w;
+    } else if constexpr (D == 128) {
+      const u32x2 w = *reinterpret_cast<const u32x2*>(p);
+      c.v[e][0] = w.x; c.v[e][1] = w.y;
+    } else {
+      c.v[e][0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+  }
+}
+
+__device__ __forceinline__ float max_over_groups(float x) {
+  x = __builtin_fmaxf(x, __shfl_xor(x, 16));
+  return __builtin_fmaxf(x, __shfl_xor(x, 32));
+}
+
+__device__ __forceinline__ float sum_over_groups(float x) {
+  x += __shfl_xor(x, 16);
+  return x + __shfl_xor(x, 32);
+}
+
+template <bool BF16>
+__device__ __forceinline__ f32x4 mfma16(u32x4 x, u32x4 y, f32x4 c) {
+  if constexpr (BF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
+}
+
+// State of a wavefront over one segment: NQ column tiles of 16 query rows.
+template <int D, int NQ>
+struct State {
+  u32x4 q[NQ][D / 32];
+  f32x4 acc[NQ][D / 16];  // acc[.][t][i]: dim (4 g + i) * (D / 16) + t
+  float m[NQ], l[NQ];     // l: this lane's keys only
+  Row row[NQ];
+  int32_t lo_all, hi_all;  // positions every row of the tile sees: [lo_all, hi_all)
+};
+
+template <int D, bool BF16, int NQ>
+__device__ __forceinline__ void step(const AttnArgs& a, const Request& rq, const Codes<D>& c, int32_t slot,
+                                     int32_t j0, float mul, float inv_cap, int lane, State<D, NQ>& s) {
+  const int g = lane >> 4;
+  f32x4 x[2][NQ];
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) x[t][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const u32x2 lo = decode_key<BF16>(c.k[t][j][2 * h]);
+        const u32x2 hi = decode_key<BF16>(c.k[t][j][2 * h + 1]);
+        const u32x4 k = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) x[t][n] = mfma16<BF16>(k, s.q[n][2 * j + h], x[t][n]);
+      }
+
+  // wave-uniform: every position of the step is in the cache and seen by every row of the tile
+  const uint64_t in_cache = __ballot(slot >= 0);
+  const bool whole = in_cache == ~0ull && j0 >= s.lo_all && j0 + kStep <= s.hi_all;
+  if (a.cap > 0.0f || a.slopes) {
+    if (a.cap > 0.0f) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[t][n][i] = capped(x[t][n][i] * mul, a.cap, inv_cap) * kLog2e;
+    } else {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) x[t][n] *= mul * kLog2e;
+    }
+    if (a.slopes) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int32_t kp = key_position(a, rq, j0 + 16 * t + 4 * g + i);
+#pragma unroll
+          for (int n = 0; n < NQ; ++n)
+            x[t][n][i] = __builtin_fmaf(s.row[n].slope, (float)(kp - s.row[n].pos), x[t][n][i]);
+        }
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) x[t][n] *= mul * kLog2e;
+  }
+  uint32_t seen[NQ];
+  if (!whole) {
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) seen[n] = 0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int o = 16 * t + 4 * g + i;
+        const bool there = (in_cache >> o) & 1;
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          const bool see = there && sees(a, s.row[n], rq, j0 + o);
+          seen[n] |= see ? 1u << (4 * t + i) : 0u;
+          x[t][n][i] = see ? x[t][n][i] : -__builtin_inff();
+        }
+      }
+  }
+
+  u32x4 p[NQ];
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    float top = x[0][n][0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) top = __builtin_fmaxf(top, x[i >> 2][n][i & 3]);
+    if (__any(top > s.m[n] + kSlack)) {
+      const float m = __builtin_fmaxf(s.m[n], max_over_groups(top));
+      const float f = exp2_of(s.m[n] - m);
+      s.m[n] = m;
+      s.l[n] *= f;
+#pragma unroll
+      for (int t = 0; t < D / 16; ++t) s.acc[n][t] *= f;
+    }
+    float e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = exp2_of(x[i >> 2][n][i & 3] - s.m[n]);
+    s.l[n] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+    p[n] = u32x4{pack_f16(e[0], e[1]), pack_f16(e[2], e[3]), pack_f16(e[4], e[5]), pack_f16(e[6], e[7])};
+  }
+
+  // values of positions outside the cache count as zeros; a NaN code in a position that only some
+  // rows see must reach those rows alone, which a product with 0 would not give
+  uint32_t v[8][D / 64];
+  bool nans = false;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+#pragma unroll
+    for (int d = 0; d < D / 64; ++d) v[e][d] = c.v[e][d];
+  if (!whole) {
+    uint32_t bad = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const bool there = (in_cache >> (16 * (e >> 2) + 4 * g + (e & 3))) & 1;
+#pragma unroll
+      for (int d = 0; d < D / 64; ++d) {
+        v[e][d] = there ? v[e][d] : 0u;
+        bad |= nan_codes(v[e][d]);
+      }
+    }
+    nans = __any(bad != 0);
+  }
+  if (nans) {
+    // count, for each output, the NaN codes its row sees: 0/1 products, exact
+    u32x4 one[NQ];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        one[n][i] = ((seen[n] >> (2 * i)) & 1 ? 0x3C00u : 0u) | ((seen[n] >> (2 * i + 1)) & 1 ? 0x3C000000u : 0u);
+#pragma unroll
+    for (int d = 0; d < D / 64; ++d)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        u32x4 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t n0 = (nan_codes(v[2 * i][d]) >> (8 * b)) & 0x80u;
+          const uint32_t n1 = (nan_codes(v[2 * i + 1][d]) >> (8 * b)) & 0x80u;
+          w[i] = (n0 ? 0x3C00u : 0u) | (n1 ? 0x3C000000u : 0u);
+        }
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          const f32x4 cnt = mfma16<false>(w, one[n], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (cnt[i] > 0.0f) s.acc[n][4 * d + b][i] = __builtin_nanf("");
+        }
+      }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+#pragma unroll
+      for (int d = 0; d < D / 64; ++d) v[e][d] &= ~((nan_codes(v[e][d]) >> 7) * 0xFFu);
+  }
+#pragma unroll
+  for (int d = 0; d < D / 64; ++d) {
+    uint32_t a0[4], a1[4], t0[4], t1[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a0[i] = v[i][d];
+      a1[i] = v[4 + i][d];
+    }
+    transpose4(a0, t0);
+    transpose4(a1, t1);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const u32x2 lo = decode_f16(t0[b]), hi = decode_f16(t1[b]);
+      const u32x4 w = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) s.acc[n][4 * d + b] = mfma16<false>(w, p[n], s.acc[n][4 * d + b]);
+    }
+  }
+}
+
+template <int D, bool BF16, int NQ>
+__device__ __forceinline__ void segment(const AttnArgs& a, const Segment& sg, bool split, float* lds) {
+  constexpr int kRows = 16 * NQ;
+  constexpr int kPitch = D + 4;  // floats; 16 bytes a row apart, so a store's 8 lanes differ in banks
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int g = lane >> 4, d16 = lane & 15;
+  const Request rq = request_of(a, sg.r);
+  State<D, NQ> s;
+  const float mul = a.scale * *a.ks;
+  const float inv_cap = a.cap > 0.0f ? 1.0f / a.cap : 0.0f;
+
+  int32_t lo_min = 0x7FFFFFFF, hi_max = 0, lo_max = 0, hi_min = 0x7FFFFFFF;
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    const Row w = row_of(a, sg.r, rq, sg.kv_head, (uint32_t)(sg.tile * kRows + 16 * n + d16));
+    s.row[n] = w;
+    s.m[n] = kNoScore;
+    s.l[n] = 0.0f;
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t) s.acc[n][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const uint16_t* qp = a.q + (int64_t)w.token * a.q_ts + (int64_t)w.head * a.q_hs + g * 16;
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j)
+      s.q[n][j] = w.token >= 0 ? *reinterpret_cast<const u32x4*>(qp + 64 * (j >> 1) + 8 * (j & 1)) : u32x4{0, 0, 0, 0};
+    if (w.token >= 0) {
+      // a tree's rows see at most the request's keys, and below ctx all of them
+      lo_min = min(lo_min, w.lo);
+      hi_max = max(hi_max, a.tree ? rq.len : w.hi);
+      lo_max = max(lo_max, w.lo);
+      hi_min = min(hi_min, w.hi);
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) {
+    lo_min = min(lo_min, __shfl_xor(lo_min, d));
+    hi_max = max(hi_max, __shfl_xor(hi_max, d));
+    lo_max = max(lo_max, __shfl_xor(lo_max, d));
+    hi_min = min(hi_min, __shfl_xor(hi_min, d));
+  }
+  s.lo_all = __builtin_amdgcn_readfirstlane(lo_max);
+  s.hi_all = __builtin_amdgcn_readfirstlane(hi_min);
+  lo_min = __builtin_amdgcn_readfirstlane(lo_min);
+  hi_max = __builtin_amdgcn_readfirstlane(hi_max);
+  if (hi_max > rq.len) hi_max = rq.len;
+  int32_t u0 = sg.u0, u1 = sg.u1;
+  if (lo_min >= hi_max) {
+    u1 = u0;
+  } else {
+    u0 = max(u0, lo_min / kUnit);
+    u1 = min(u1, (hi_max + kUnit - 1) / kUnit);
+  }
+
+  const int32_t* table_row = a.table + (int64_t)sg.r * a.table_ld;
+  const uint8_t* kbase = a.kc + (int64_t)sg.kv_head * D;
+  const uint8_t* vbase = a.vc + (int64_t)sg.kv_head * D;
+  const int32_t off = wave * kStep + (lane & 31);
+  if (u0 < u1) {
+    int32_t s0 = slot_at(a, table_row, hi_max, u0 * kUnit + off);
+    int32_t s1 = u0 + 1 < u1 ? slot_at(a, table_row, hi_max, (u0 + 1) * kUnit + off) : -1;
+    Codes<D> c0, c1;
+    load_codes<D>(a, s0, kbase, vbase, lane, c0);
+    for (int32_t u = u0; u < u1; u += 2) {
+      int32_t s2 = -1, s3 = -1;
+      if (u + 1 < u1) load_codes<D>(a, s1, kbase, vbase, lane, c1);
+      if (u + 2 < u1) s2 = slot_at(a, table_row, hi_max, (u + 2) * kUnit + off);
+      step<D, BF16, NQ>(a, rq, c0, s0, u * kUnit + wave * kStep, mul, inv_cap, lane, s);
+      if (u + 1 >= u1) break;
+      if (u + 2 < u1) load_codes<D>(a, s2, kbase, vbase, lane, c0);
+      if (u + 3 < u1) s3 = slot_at(a, table_row, hi_max, (u + 3) * kUnit + off);
+      step<D, BF16, NQ>(a, rq, c1, s1, (u + 1) * kUnit + wave * kStep, mul, inv_cap, lane, s);
+      s0 = s2;
+      s1 = s3;
+    }
+  }
+
+  // join the wavefronts
+  float* ml = lds + kWaves * 16 * kPitch;  // [wave][kRows][2]
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    const float l = sum_over_groups(s.l[n]);
+    if (g == 0) {
+      ml[(wave * kRows + 16 * n + d16) * 2] = s.m[n];
+      ml[(wave * kRows + 16 * n + d16) * 2 + 1] = l;
+    }
+  }
+  const float vs = *a.vs;
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    __syncthreads();
+    float m = kNoScore;
+#pragma unroll
+    for (int k = 0; k < kWaves; ++k) m = __builtin_fmaxf(m, ml[(k * kRows + 16 * n + d16) * 2]);
+    const float f = exp2_of(s.m[n] - m);
+    float* mine = lds + (wave * 16 + d16) * kPitch + g * (D / 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int t = 0; t < D / 16; t += 4) {
+        f32x4 o = {s.acc[n][t][i], s.acc[n][t + 1][i], s.acc[n][t + 2][i], s.acc[n][t + 3][i]};
+        *reinterpret_cast<f32x4*>(mine + i * (D / 16) + t) = o * f;
+      }
+    __syncthreads();
+    // 16 threads a row, D / 16 contiguous dims each
+    const int row = tid >> 4, part = tid & 15;
+    float mr = kNoScore, lr = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kWaves; ++k) mr = __builtin_fmaxf(mr, ml[(k * kRows + 16 * n + row) * 2]);
+#pragma unroll
+    for (int k = 0; k < kWaves; ++k)
+      lr += ml[(k * kRows + 16 * n + row) * 2 + 1] * exp2_of(ml[(k * kRows + 16 * n + row) * 2] - mr);
+    float o[D / 16];
+#pragma unroll
+    for (int t = 0; t < D / 16; t += 4) {
+      f32x4 sum = *reinterpret_cast<f32x4*>(lds + row * kPitch + part * (D / 16) + t);
+#pragma unroll
+      for (int k = 1; k < kWaves; ++k)
+        sum += *reinterpret_cast<f32x4*>(lds + (k * 16 + row) * kPitch + part * (D / 16) + t);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[t + i] = sum[i];
+    }
+    const uint32_t rr = (uint32_t)(sg.tile * kRows + 16 * n + row);
+    if (rr < (uint32_t)rq.count * a.group.d) {
+      if (split && !(sg.first && sg.last)) {
+        const int64_t at = part_slot(blockIdx.x, sg.first) * kRows + 16 * n + row;
+        float* op = a.part + at * D + part * (D / 16);
+#pragma unroll
+        for (int t = 0; t < D / 16; t += 4) *reinterpret_cast<f32x4*>(op + t) = f32x4{o[t], o[t + 1], o[t + 2], o[t + 3]};
+        if (part == 0) *reinterpret_cast<f32x2*>(a.part_ml + 2 * at) = f32x2{mr, lr};
+      } else {
+        const int32_t i = (int32_t)div_of(rr, a.group);
+        const int32_t head = sg.kv_head * (int32_t)a.group.d + (int32_t)(rr - (uint32_t)i * a.group.d);
+        const float inv = lr == 0.0f ? 0.0f : vs / lr;
+        uint16_t* op = a.out + (int64_t)(rq.start + i) * a.out_ts + (int64_t)head * a.out_hs + part * (D / 16);
+#pragma unroll
+        for (int t = 0; t < D / 16; t += 4)
+          *reinterpret_cast<u32x2*>(op + t) = u32x2{pack_out<BF16>(o[t] * inv, o[t + 1] * inv), pack_out<BF16>(o[t + 2] * inv, o[t + 3] * inv)};
+      }
+    }
+  }
+  __syncthreads();  // the next segment writes ml and the tiles again
+}
+
+template <int D, bool BF16, int NQ>
+__global__ void __launch_bounds__(kThreads) attention_stream_kernel(AttnArgs a) {
+  constexpr int kRows = 16 * NQ;
+  __shared__ __align__(16) float lds[kWaves * 16 * (D + 4) + kWaves * kRows * 2];
+  if (a.workers == 0) {
+    Segment s;
+    s.kv_head = blockIdx.x;
+    s.r = blockIdx.y;
+    s.first = s.last = true;
+    s.last_worker = 0;
+    const Request q = request_of(a, s.r);
+    s.u0 = 0;
+    s.u1 = (q.len + kUnit - 1) / kUnit;
+    const int32_t tiles = (int32_t)(((uint32_t)q.count * a.group.d + kRows - 1) / kRows);
+    for (s.tile = blockIdx.z; s.tile < tiles; s.tile += gridDim.z) segment<D, BF16, NQ>(a, s, false, lds);
+    return;
+  }
+  __shared__ uint64_t scratch[kThreads / 64 + 2];
+  Share<kThreads> share;
+  share.begin(a, kRows, kUnit, scratch);
+  Segment s;
+  Header h{0, 0, 0, -1};
+  while (share.next(a, s)) {
+    if (s.first && !s.last) h = Header{s.r, s.tile, s.kv_head, s.last_worker};
+    segment<D, BF16, NQ>(a, s, true, lds);
+  }
+  if (threadIdx.x == 0) *reinterpret_cast<Header*>(a.headers + 4 * blockIdx.x) = h;
+}
+
+// Joins the pieces of the items that were shared out: block (w, y) takes four rows of the item that
+// begins in worker w and ends in worker last_worker, a wavefront each.  The pieces are summed in the
+// workers' order, whatever order they were computed in.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads) attention_join_kernel(AttnArgs a, int32_t rows) {
+  const Header h = *reinterpret_cast<const Header*>(a.headers + 4 * blockIdx.x);
+  if (h.last_worker < 0) return;
+  const Request rq = request_of(a, h.r);
+  const int lane = threadIdx.x & 63;
+  const int32_t local = blockIdx.y * kWaves + (threadIdx.x >> 6);
+  const uint32_t rr = (uint32_t)(h.tile * rows + local);
+  if (rr >= (uint32_t)rq.count * a.group.d) return;
+  const uint32_t w0 = blockIdx.x;
+  const int32_t n = h.last_worker - (int32_t)w0 + 1;
+  constexpr int E = D / 64;
+  float m = kNoScore;
+  for (int32_t k = lane; k < n; k += 64) m = __builtin_fmaxf(m, a.part_ml[2 * (part_slot(w0 + k, k == 0) * rows + local)]);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) m = __builtin_fmaxf(m, __shfl_xor(m, d));
+  float o[E], l = 0.0f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.0f;
+  for (int32_t b = 0; b < n; b += 64) {
+    float f = 0.0f, lk = 0.0f;
+    if (b + lane < n) {
+      const f32x2 v = *reinterpret_cast<const f32x2*>(a.part_ml + 2 * (part_slot(w0 + b + lane, b + lane == 0) * rows + local));
+      f = exp2_of(v.x - m);
+      lk = v.y * f;
+    }
+    const int32_t c = min(64, n - b);
+#pragma unroll 8
+    for (int32_t k = 0; k < c; ++k) {
+      const float* p = a.part + (part_slot(w0 + b + k, b + k == 0) * rows + local) * D + lane * E;
+      const float fk = __shfl(f, k);
+      l += __shfl(lk, k);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = __builtin_fmaf(p[e], fk, o[e]);
+    }
+  }
+  const float inv = l == 0.0f ? 0.0f : *a.vs / l;
+  const int32_t i = (int32_t)div_of(rr, a.group);
+  const int32_t head = h.kv_head * (int32_t)a.group.d + (int32_t)(rr - (uint32_t)i * a.group.d);
+  uint16_t* op = a.out + (int64_t)(rq.start + i) * a.out_ts + (int64_t)head * a.out_hs + lane * E;
+  if constexpr (E == 1) {
+    *op = (uint16_t)pack_out<BF16>(o[0] * inv, 0.0f);
+  } else if constexpr (E == 2) {
+    *reinterpret_cast<uint32_t*>(op) = pack_out<BF16>(o[0] * inv, o[1] * inv);
+  } else {
+    *reinterpret_cast<u32x2*>(op) = u32x2{pack_out<BF16>(o[0] * inv, o[1] * inv), pack_out<BF16>(o[2] * inv, o[3] * inv)};
+  }
+}
+
+template <int D, bool BF16, int NQ>
+void launch_stream(const AttnArgs& a, hipStream_t stream) {
+  const dim3 grid = a.workers ? dim3((uint32_t)a.workers) : dim3((uint32_t)a.kv_heads, (uint32_t)a.requests, (uint32_t)a.row_tiles);
+  hipLaunchKernelGGL((attention_stream_kernel<D, BF16, NQ>), grid, dim3(kThreads), 0, stream, a);
+}
+
+template <int D, bool BF16>
+hipError_t launch_all(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
+  switch (p.kernel) {
+    case AttnKernel::Stream16: launch_stream<D, BF16, 1>(a, stream); break;
+    case AttnKernel::Stream32: launch_stream<D, BF16, 2>(a, stream); break;
+    case AttnKernel::Stream64:
+      if constexpr (D <= 128) launch_stream<D, BF16, 4>(a, stream);
+      break;
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.workers == 0) return e;
+  hipLaunchKernelGGL((attention_join_kernel<D, BF16>), dim3((uint32_t)a.workers, (uint32_t)(p.rows / kWaves)),
+                     dim3(kThreads), 0, stream, a, p.rows);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+AttnPlan plan_attention(int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t requests,
+                        int64_t max_query_len, int64_t max_seq_len) {
+  AttnPlan p{};
+  const int64_t rows = max_query_len * (heads / kv_heads);
+  if (rows <= 16) {
+    p.kernel = AttnKernel::Stream16;
+    p.rows = 16;
+  } else if (rows <= 32 || head_dim > 128) {
+    p.kernel = AttnKernel::Stream32;
+    p.rows = 32;
+  } else {
+    p.kernel = AttnKernel::Stream64;
+    p.rows = 64;
+  }
+  const int64_t items = requests * kv_heads * ((rows + p.rows - 1) / p.rows);
+  if (max_seq_len > 2 * kUnit && items < 4 * kComputeUnits) p.workers = 2 * kComputeUnits;
+  if (p.workers)
+    p.workspace = (int64_t)p.workers * (2 * (int64_t)p.rows * (head_dim + 2) + 4) * (int64_t)sizeof(float);
+  return p;
+}
+
+hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, int head_dim, bool bf16,
+                            hipStream_t stream) {
+  switch (head_dim) {
+    case 64: return bf16 ? launch_all<64, true>(a, p, stream) : launch_all<64, false>(a, p, stream);
+    case 128: return bf16 ? launch_all<128, true>(a, p, stream) : launch_all<128, false>(a, p, stream);
+    default: return bf16 ? launch_all<256, true>(a, p, stream) : launch_all<256, false>(a, p, stream);
+  }
+}
+
+}  // namespace nvfp4

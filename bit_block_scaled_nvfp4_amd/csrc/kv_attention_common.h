@@ -1,0 +1,361 @@
+// Device code shared by the attention kernels over the paged FP8 cache (gfx950): which part of the
+// work a workgroup takes, which positions a query row sees, how scores are capped and biased, and how
+// partial results of one row tile are kept and joined.
+//
+// Terms.  Query rows of one request and one KV head are numbered row = i * group + g (token i, head
+// g of the group of query heads that share the KV head), so that all rows of a tile read the same
+// keys.  An item is one (request, row tile, KV head); its keys are counted in units (a fixed number
+// of positions, aligned at position 0).
+//
+// All exponentials are base 2: scores are multiplied by log2(e) once.  The softmax keeps a reference
+// value m per row instead of the exact running maximum: m is raised (and what is accumulated so far
+// scaled down) only when a score exceeds it by more than kSlack, so exp2(x - m) stays below
+// 2^kSlack = 256, far inside FP16, and the accumulators are not rescaled on most tiles.
+#pragma once
+
+#include "attention_internal.h"
+
+namespace nvfp4 {
+namespace attn {
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kSlack = 8.0f;
+// Reference of a row that has seen nothing: below every finite score that FP32 sums of real keys
+// reach, and finite, so that exp2(-inf - m) is 0 and not NaN.
+constexpr float kNoScore = -1e37f;
+
+__device__ __forceinline__ uint32_t div_of(uint32_t n, const FastDiv& f) {
+  return (uint32_t)(((uint64_t)n * f.mul) >> f.shift);
+}
+
+__device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// ---- which positions a row sees -------------------------------------------------------------
+
+// One query row as a lane holds it.  Visible: lo <= j < hi, or (drafted trees) hi <= j and the
+// row's bit of j - ctx set.
+struct Row {
+  int32_t lo, hi;
+  int32_t pos;    // position for the distance bias
+  int32_t token;  // row of q, or -1 where the tile has no such row
+  int32_t head;
+  float slope;    // times log2(e); 0 without a bias
+};
+
+struct Request {
+  int32_t start, count;  // query rows
+  int32_t len, ctx;      // positions in the cache; len - count
+};
+
+__device__ __forceinline__ Request request_of(const AttnArgs& a, int32_t r) {
+  Request q;
+  int32_t s = a.query_start[r], e = a.query_start[r + 1];
+  s = s < 0 ? 0 : (s > a.tokens ? a.tokens : s);
+  e = e < s ? s : (e > a.tokens ? a.tokens : e);
+  q.start = s;
+  q.count = e - s;
+  const int32_t l = a.seq_lens[r];
+  q.len = l > 0 ? l : 0;
+  q.ctx = q.len - q.count;
+  return q;
+}
+
+__device__ __forceinline__ Row row_of(const AttnArgs& a, int32_t r, const Request& q, int32_t kv_head,
+                                      uint32_t row) {
+  Row w;
+  w.lo = 0;
+  w.hi = 0;
+  w.pos = 0;
+  w.token = -1;
+  w.head = 0;
+  w.slope = 0.0f;
+  if (row >= (uint32_t)q.count * a.group.d) return w;  // tokens * heads < 2^31
+  const int32_t i = (int32_t)div_of(row, a.group);
+  w.token = q.start + i;
+  w.head = kv_head * (int32_t)a.group.d + (int32_t)(row - (uint32_t)i * a.group.d);
+  w.pos = q.ctx + i;
+  if (a.slopes) w.slope = a.slopes[w.head] * kLog2e;
+  if (a.tree) {
+    w.hi = q.ctx > 0 ? q.ctx : 0;
+    if (a.slopes && a.positions) w.pos = a.positions[w.token];
+  } else {
+    int32_t end = w.pos + 1;
+    if (a.prefix_lens) {
+      const int32_t p = a.prefix_lens[r];
+      end = end > p ? end : p;
+    }
+    w.hi = end < 0 ? 0 : (end > q.len ? q.len : end);
+    if (a.doc_start) {
+      const int32_t s = a.doc_start[w.token];
+      w.lo = s > 0 ? s : 0;
+    }
+  }
+  return w;
+}
+
+// Whether row w sees position j < len (drafted trees: through the row's own mask bits).
+__device__ __forceinline__ bool sees(const AttnArgs& a, const Row& w, const Request& q, int32_t j) {
+  if (j < w.hi) return j >= w.lo;
+  if (!a.tree || w.token < 0 || j >= q.len) return false;
+  const int32_t d = j - q.ctx;  // >= 0: j >= hi >= ctx
+  if ((d >> 6) >= a.tree_words) return false;
+  return (a.tree[(int64_t)w.token * a.tree_ld + (d >> 6)] >> (d & 63)) & 1;
+}
+
+// Position at which key j counts in the distance bias.
+__device__ __forceinline__ int32_t key_position(const AttnArgs& a, const Request& q, int32_t j) {
+  if (!a.tree || !a.positions || j < q.ctx || j >= q.len) return j;
+  return a.positions[q.start + (j - q.ctx)];
+}
+
+// Score of a raw product x: capped and biased, in units of log2 (x is already times scale * key
+// scale here).  tanh(y) = 1 - 2 / (exp(2 y) + 1): its error is a few 2^-24, times the cap.
+__device__ __forceinline__ float capped(float x, float cap, float inv_cap) {
+  const float e = exp2_of(x * inv_cap * (2.0f * kLog2e));
+  return __builtin_fmaf(-2.0f * cap, __builtin_amdgcn_rcpf(e + 1.0f), cap);
+}
+
+// ---- cache rows -----------------------------------------------------------------------------
+
+// Slot of position j of request r, or -1 where it is not in the cache.  j may be any value.
+__device__ __forceinline__ int32_t slot_at(const AttnArgs& a, const int32_t* table_row, int32_t len,
+                                           int32_t j) {
+  if (j < 0 || j >= len) return -1;
+  const uint32_t col = div_of((uint32_t)j, a.bs);
+  if (col >= (uint32_t)a.table_width) return -1;
+  const int32_t b = table_row[col];
+  const int64_t s = (int64_t)b * a.bs.d + ((uint32_t)j - col * a.bs.d);
+  return (b >= 0 && s < a.num_slots) ? (int32_t)s : -1;
+}
+
+// Non-zero where one of the four codes is NaN (0x7F or 0xFF).
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+
+// 4 x 4 byte transpose: out[t] holds byte t of in[0 .. 3].
+__device__ __forceinline__ void transpose4(const uint32_t in[4], uint32_t out[4]) {
+  const uint32_t p0 = __builtin_amdgcn_perm(in[1], in[0], 0x05010400u);
+  const uint32_t p1 = __builtin_amdgcn_perm(in[1], in[0], 0x07030602u);
+  const uint32_t q0 = __builtin_amdgcn_perm(in[3], in[2], 0x05010400u);
+  const uint32_t q1 = __builtin_amdgcn_perm(in[3], in[2], 0x07030602u);
+  out[0] = __builtin_amdgcn_perm(q0, p0, 0x05040100u);
+  out[1] = __builtin_amdgcn_perm(q0, p0, 0x07060302u);
+  out[2] = __builtin_amdgcn_perm(q1, p1, 0x05040100u);
+  out[3] = __builtin_amdgcn_perm(q1, p1, 0x07060302u);
+}
+
+// Four codes as four 16-bit values (exact: every E4M3 value is an FP16 and a BF16 value).
+__device__ __forceinline__ u32x2 decode_f16(uint32_t w) {
+  u32x2 o;
+  o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w, 1.0f, false));
+  o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w, 1.0f, true));
+  return o;
+}
+
+__device__ __forceinline__ u32x2 decode_bf16(uint32_t w) {
+  u32x2 o;
+  o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, 1.0f, false));
+  o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, 1.0f, true));
+  return o;
+}
+
+// Keys are decoded to the query's type, values to FP16.
+template <bool BF16>
+__device__ __forceinline__ u32x2 decode_key(uint32_t w) {
+  if constexpr (BF16) return decode_bf16(w);
+  return decode_f16(w);
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  f16x2 p;
+  p[0] = (_Float16)a;
+  p[1] = (_Float16)b;
+  return __builtin_bit_cast(uint32_t, p);
+}
+
+// One output element in the query's type, rounded to nearest even.
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack_out(float a, float b) {
+  if constexpr (BF16) {
+    bf16x2 p;
+    p[0] = (__bf16)a;
+    p[1] = (__bf16)b;
+    return __builtin_bit_cast(uint32_t, p);
+  }
+  return pack_f16(a, b);
+}
+
+// ---- division of the work -------------------------------------------------------------------
+
+// A stretch of one item's key units.
+struct Segment {
+  int32_t r, tile, kv_head;
+  int32_t u0, u1;    // units
+  bool first, last;  // it holds the item's first / last unit
+  int32_t last_worker;  // worker that holds the item's last unit
+};
+
+// Headers that the workers leave for the joining kernel.
+struct Header {
+  int32_t r, tile, kv_head;
+  int32_t last_worker;  // of the item that begins in this worker and ends in a later one, else -1
+};
+
+// Work of request r in units, all its items: every item counts the units of the whole request.  (An
+// item of a prompt whose rows see less skips the rest; such calls are divided by row tiles unless
+// the new tokens are few beside their context.)
+__device__ __forceinline__ void weight_of(const AttnArgs& a, int32_t r, int32_t rows, int32_t unit,
+                                          uint32_t& units, uint64_t& total) {
+  const Request q = request_of(a, r);
+  const uint64_t tiles = ((uint64_t)q.count * a.group.d + rows - 1) / (uint32_t)rows;
+  units = ((uint32_t)q.len + (uint32_t)unit - 1) / (uint32_t)unit;
+  if (units == 0) units = 1;  // the rows still get their zeros
+  total = (uint64_t)units * tiles * (uint32_t)a.kv_heads;
+}
+
+__device__ __forceinline__ uint64_t shfl_up64(uint64_t x, int d) {
+  const uint32_t lo = __shfl_up((uint32_t)x, d), hi = __shfl_up((uint32_t)(x >> 32), d);
+  return (uint64_t)hi << 32 | lo;
+}
+
+// The workers' shares: worker w takes units [W w / P, W (w + 1) / P) of the W units of all items, one
+// after another.  Every workgroup finds its own start by summing the requests' weights (two passes
+// over the lengths, NT requests at a time), with no launch before it and nothing kept.  scratch: 3 +
+// NT / 64 words of 64 bits in LDS.
+template <int NT>
+struct Share {
+  uint64_t W, x, end;    // all units; the next unit and the end of this worker's share
+  uint64_t base;         // units before request r
+  uint32_t units;        // of an item of request r
+  uint64_t total;        // of request r
+  int32_t r, rows, unit;
+  uint32_t P, w;
+
+  __device__ __forceinline__ void begin(const AttnArgs& a, int32_t rows_, int32_t unit_, uint64_t* scratch) {
+    rows = rows_;
+    unit = unit_;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    constexpr int kW = NT / 64;
+    const int R = a.requests;
+    uint64_t sum = 0;
+    uint64_t mine = 0;  // inclusive sum up to this thread's request, where R <= NT
+    uint64_t own = 0;
+    for (int b = 0; b < R; b += NT) {
+      const int i = b + tid;
+      uint64_t t = 0;
+      uint32_t u = 0;
+      if (i < R) weight_of(a, i, rows, unit, u, t);
+      own = t;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const uint64_t p = shfl_up64(t, d);
+        if (lane >= d) t += p;
+      }
+      if (lane == 63) scratch[wave] = t;
+      __syncthreads();
+      uint64_t before = sum;
+      for (int k = 0; k < kW; ++k) {
+        if (k < wave) before += scratch[k];
+        sum += scratch[k];
+      }
+      mine = before + t;
+      __syncthreads();
+    }
+    W = sum;
+    // a worker takes two units at least: the smallest shares cost more to join than to compute
+    const uint64_t most = (W + 1) / 2;
+    P = (uint32_t)(most < (uint64_t)a.workers ? (most > 0 ? most : 1) : (uint64_t)a.workers);
+    w = blockIdx.x;
+    if (w >= P) {
+      x = end = 0;
+      return;
+    }
+    x = W * w / P;
+    end = W * (w + 1) / P;
+    if (x >= end) return;
+    // the request that holds unit x
+    if (R <= NT) {
+      if (tid < R && mine > x && mine - own <= x) {
+        scratch[kW] = mine - own;
+        scratch[kW + 1] = (uint64_t)tid;
+      }
+      __syncthreads();
+    } else {
+      uint64_t s = 0;
+      for (int b = 0; b < R; b += NT) {
+        const int i = b + tid;
+        uint64_t t = 0;
+        uint32_t u = 0;
+        if (i < R) weight_of(a, i, rows, unit, u, t);
+        const uint64_t o = t;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+          const uint64_t p = shfl_up64(t, d);
+          if (lane >= d) t += p;
+        }
+        if (lane == 63) scratch[wave] = t;
+        __syncthreads();
+        uint64_t before = s;
+        for (int k = 0; k < kW; ++k) {
+          if (k < wave) before += scratch[k];
+          s += scratch[k];
+        }
+        const uint64_t incl = before + t;
+        if (i < R && incl > x && incl - o <= x) {
+          scratch[kW] = incl - o;
+          scratch[kW + 1] = (uint64_t)i;
+        }
+        __syncthreads();
+        if (s > x) break;  // uniform: s is the same in every thread
+      }
+    }
+    base = scratch[kW];
+    r = (int32_t)scratch[kW + 1];
+    weight_of(a, r, rows, unit, units, total);
+  }
+
+  // The next segment, or false when the share is done.  Uniform over the workgroup.
+  __device__ __forceinline__ bool next(const AttnArgs& a, Segment& s) {
+    if (x >= end) return false;
+    while (x >= base + total) {  // ends before r leaves the requests: x < W = the sum of all totals
+      base += total;
+      ++r;
+      weight_of(a, r, rows, unit, units, total);
+    }
+    const uint64_t y = x - base;
+    const uint64_t item = y / units;
+    const uint32_t off = (uint32_t)(y - item * units);
+    uint64_t n = units - off;
+    if (n > end - x) n = end - x;
+    s.r = r;
+    s.tile = (int32_t)(item / (uint32_t)a.kv_heads);
+    s.kv_head = (int32_t)(item - (uint64_t)s.tile * (uint32_t)a.kv_heads);
+    s.u0 = (int32_t)off;
+    s.u1 = (int32_t)(off + n);
+    s.first = off == 0;
+    s.last = off + n == units;
+    const uint64_t tail = base + (item + 1) * units;  // one past the item's last unit
+    // worker of unit tail - 1: the largest w with W w / P <= tail - 1, that is W w < tail P
+    s.last_worker = (int32_t)((tail * P - 1) / W);
+    x += n;
+    return true;
+  }
+};
+
+// Partial results: worker w keeps two slots, 2 w for a segment that continues an item of an earlier
+// worker and 2 w + 1 for one whose item goes on in a later one.
+__device__ __forceinline__ int64_t part_slot(uint32_t w, bool first) { return 2 * (int64_t)w + (first ? 1 : 0); }
+
+}  // namespace attn
+}  // namespace nvfp4
