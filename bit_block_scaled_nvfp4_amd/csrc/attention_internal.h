@@ -46,6 +46,7 @@ enum class AttnKernel : int32_t {
   Stream16,  // a wavefront streams its own keys past 16, 32 or 64 query rows
   Stream32,
   Stream64,
+  Tiled,  // key tiles staged in LDS for 256 query rows
 };
 
 struct AttnPlan {
@@ -94,5 +95,6 @@ hipError_t launch_block_tables(const TablesArgs& a, hipStream_t stream);
 // Launch the plan's kernel (and, with workers, the joining kernel).
 hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, int head_dim, bool bf16,
                             hipStream_t stream);
+hipError_t launch_attention_tiled(const AttnArgs& a, int head_dim, bool bf16, hipStream_t stream);
 
 }  // namespace nvfp4

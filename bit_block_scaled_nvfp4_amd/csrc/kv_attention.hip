@@ -94,7 +94,8 @@ struct State {
 };
 
 template <int D, bool BF16, int NQ>
-__device__ __forceinline__ void step(const AttnArgs& a, const Request& rq, const Codes<D>& c, int32_t slot,
+__device__ __forceinline__ void step(const AttnArgs& a, const Request& rq, Codes<D>& c, int32_t slot,
+                                     const uint8_t* vbase,
                                      int32_t j0, float mul, float inv_cap, int lane, State<D, NQ>& s) {
   const int g = lane >> 4;
   f32x4 x[2][NQ];
@@ -149,23 +150,17 @@ __device__ __forceinline__ void step(const AttnArgs& a, const Request& rq, const
 #pragma unroll
       for (int n = 0; n < NQ; ++n) x[t][n] *= mul * kLog2e;
   }
+  // bit 16 t + i of seen[n] >> 4 g: whether row n sees position 16 t + 4 g + i of the step
   uint32_t seen[NQ];
   if (!whole) {
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) seen[n] = 0;
+    for (int n = 0; n < NQ; ++n) {
+      seen[n] = ((uint32_t)sees64(a, s.row[n], rq, j0) & (uint32_t)in_cache) >> (4 * g);
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int o = 16 * t + 4 * g + i;
-        const bool there = (in_cache >> o) & 1;
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-          const bool see = there && sees(a, s.row[n], rq, j0 + o);
-          seen[n] |= see ? 1u << (4 * t + i) : 0u;
-          x[t][n][i] = see ? x[t][n][i] : -__builtin_inff();
-        }
-      }
+        for (int i = 0; i < 4; ++i) x[t][n][i] = kept(x[t][n][i], seen[n], 16 * t + i);
+    }
   }
 
   u32x4 p[NQ];
@@ -189,14 +184,10 @@ __device__ __forceinline__ void step(const AttnArgs& a, const Request& rq, const
     p[n] = u32x4{pack_f16(e[0], e[1]), pack_f16(e[2], e[3]), pack_f16(e[4], e[5]), pack_f16(e[6], e[7])};
   }
 
-  // values of positions outside the cache count as zeros; a NaN code in a position that only some
-  // rows see must reach those rows alone, which a product with 0 would not give
-  uint32_t v[8][D / 64];
+  // Values of positions outside the cache count as zeros.  A NaN code in a position that only some rows
+  // see must reach those rows alone, which a product with 0 would not give: it counts as 0 here too
+  // and the rows that see it are set to NaN afterwards.
   bool nans = false;
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-#pragma unroll
-    for (int d = 0; d < D / 64; ++d) v[e][d] = c.v[e][d];
   if (!whole) {
     uint32_t bad = 0;
 #pragma unroll
@@ -204,51 +195,25 @@ __device__ __forceinline__ void step(const AttnArgs& a, const Request& rq, const
       const bool there = (in_cache >> (16 * (e >> 2) + 4 * g + (e & 3))) & 1;
 #pragma unroll
       for (int d = 0; d < D / 64; ++d) {
-        v[e][d] = there ? v[e][d] : 0u;
-        bad |= nan_codes(v[e][d]);
+        c.v[e][d] = there ? c.v[e][d] : 0u;
+        bad |= nan_codes(c.v[e][d]);
       }
     }
     nans = __any(bad != 0);
-  }
-  if (nans) {
-    // count, for each output, the NaN codes its row sees: 0/1 products, exact
-    u32x4 one[NQ];
+    if (nans) {
 #pragma unroll
-    for (int n = 0; n < NQ; ++n)
+      for (int e = 0; e < 8; ++e)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        one[n][i] = ((seen[n] >> (2 * i)) & 1 ? 0x3C00u : 0u) | ((seen[n] >> (2 * i + 1)) & 1 ? 0x3C000000u : 0u);
-#pragma unroll
-    for (int d = 0; d < D / 64; ++d)
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        u32x4 w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t n0 = (nan_codes(v[2 * i][d]) >> (8 * b)) & 0x80u;
-          const uint32_t n1 = (nan_codes(v[2 * i + 1][d]) >> (8 * b)) & 0x80u;
-          w[i] = (n0 ? 0x3C00u : 0u) | (n1 ? 0x3C000000u : 0u);
-        }
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-          const f32x4 cnt = mfma16<false>(w, one[n], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (cnt[i] > 0.0f) s.acc[n][4 * d + b][i] = __builtin_nanf("");
-        }
-      }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-#pragma unroll
-      for (int d = 0; d < D / 64; ++d) v[e][d] &= ~((nan_codes(v[e][d]) >> 7) * 0xFFu);
+        for (int d = 0; d < D / 64; ++d) c.v[e][d] = without_nans(c.v[e][d]);
+    }
   }
 #pragma unroll
   for (int d = 0; d < D / 64; ++d) {
     uint32_t a0[4], a1[4], t0[4], t1[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      a0[i] = v[i][d];
-      a1[i] = v[4 + i][d];
+      a0[i] = c.v[i][d];
+      a1[i] = c.v[4 + i][d];
     }
     transpose4(a0, t0);
     transpose4(a1, t1);
@@ -258,6 +223,29 @@ __device__ __forceinline__ void step(const AttnArgs& a, const Request& rq, const
       const u32x4 w = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
       for (int n = 0; n < NQ; ++n) s.acc[n][4 * d + b] = mfma16<false>(w, p[n], s.acc[n][4 * d + b]);
+    }
+  }
+  if (nans) {
+#pragma unroll 1
+    for (int o = 0; o < kStep; ++o) {
+      const int32_t at = __shfl(slot, o);
+      if (at < 0) continue;
+      // this lane's dims are the D / 4 from g * D / 4 on
+      const uint8_t* p8 = vbase + (int64_t)at * a.cache_ld + g * (D / 4);
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        const bool see = ((uint32_t)sees64(a, s.row[n], rq, j0) >> o) & 1;
+#pragma unroll
+        for (int w = 0; w < D / 16; ++w) {
+          const uint32_t bad = see ? nan_codes(*reinterpret_cast<const uint32_t*>(p8 + 4 * w)) : 0u;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            constexpr int T = D / 16;
+            f32x4& o4 = s.acc[n][(4 * w + b) % T];
+            o4[(4 * w + b) / T] = __uint_as_float(__float_as_uint(o4[(4 * w + b) / T]) | ((bad >> (8 * b + 7)) & 1) * 0x7FFFFFFFu);
+          }
+        }
+      }
     }
   }
 }
@@ -327,11 +315,11 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Segment& sg, bo
       int32_t s2 = -1, s3 = -1;
       if (u + 1 < u1) load_codes<D>(a, s1, kbase, vbase, lane, c1);
       if (u + 2 < u1) s2 = slot_at(a, table_row, hi_max, (u + 2) * kUnit + off);
-      step<D, BF16, NQ>(a, rq, c0, s0, u * kUnit + wave * kStep, mul, inv_cap, lane, s);
+      step<D, BF16, NQ>(a, rq, c0, s0, vbase, u * kUnit + wave * kStep, mul, inv_cap, lane, s);
       if (u + 1 >= u1) break;
       if (u + 2 < u1) load_codes<D>(a, s2, kbase, vbase, lane, c0);
       if (u + 3 < u1) s3 = slot_at(a, table_row, hi_max, (u + 3) * kUnit + off);
-      step<D, BF16, NQ>(a, rq, c1, s1, (u + 1) * kUnit + wave * kStep, mul, inv_cap, lane, s);
+      step<D, BF16, NQ>(a, rq, c1, s1, vbase, (u + 1) * kUnit + wave * kStep, mul, inv_cap, lane, s);
       s0 = s2;
       s1 = s3;
     }
@@ -499,6 +487,11 @@ hipError_t launch_all(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) 
     case AttnKernel::Stream64:
       if constexpr (D <= 128) launch_stream<D, BF16, 4>(a, stream);
       break;
+    case AttnKernel::Tiled: {
+      const hipError_t t = launch_attention_tiled(a, D, BF16, stream);
+      if (t != hipSuccess) return t;
+      break;
+    }
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.workers == 0) return e;
@@ -516,15 +509,22 @@ AttnPlan plan_attention(int64_t heads, int64_t kv_heads, int64_t head_dim, int64
   if (rows <= 16) {
     p.kernel = AttnKernel::Stream16;
     p.rows = 16;
-  } else if (rows <= 32 || head_dim > 128) {
+  } else if (rows <= 32) {
     p.kernel = AttnKernel::Stream32;
     p.rows = 32;
-  } else {
+  } else if (rows <= 64 && head_dim <= 128) {
     p.kernel = AttnKernel::Stream64;
     p.rows = 64;
+  } else {
+    p.kernel = AttnKernel::Tiled;
+    p.rows = 256;
   }
   const int64_t items = requests * kv_heads * ((rows + p.rows - 1) / p.rows);
-  if (max_seq_len > 2 * kUnit && items < 4 * kComputeUnits) p.workers = 2 * kComputeUnits;
+  if (p.kernel == AttnKernel::Tiled) {
+    if (max_seq_len > 256 && items < kComputeUnits) p.workers = kComputeUnits;
+  } else if (max_seq_len > 2 * kUnit && items < 4 * kComputeUnits) {
+    p.workers = 2 * kComputeUnits;
+  }
   if (p.workers)
     p.workspace = (int64_t)p.workers * (2 * (int64_t)p.rows * (head_dim + 2) + 4) * (int64_t)sizeof(float);
   return p;

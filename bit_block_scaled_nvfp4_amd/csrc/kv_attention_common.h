@@ -103,13 +103,34 @@ __device__ __forceinline__ Row row_of(const AttnArgs& a, int32_t r, const Reques
   return w;
 }
 
-// Whether row w sees position j < len (drafted trees: through the row's own mask bits).
-__device__ __forceinline__ bool sees(const AttnArgs& a, const Row& w, const Request& q, int32_t j) {
-  if (j < w.hi) return j >= w.lo;
-  if (!a.tree || w.token < 0 || j >= q.len) return false;
-  const int32_t d = j - q.ctx;  // >= 0: j >= hi >= ctx
-  if ((d >> 6) >= a.tree_words) return false;
-  return (a.tree[(int64_t)w.token * a.tree_ld + (d >> 6)] >> (d & 63)) & 1;
+// Bits b of a 64-bit word with lo <= b < hi.
+__device__ __forceinline__ uint64_t bits_below(int32_t x) {
+  return x <= 0 ? 0ull : (x >= 64 ? ~0ull : (1ull << x) - 1);
+}
+
+// Which of positions j0 .. j0 + 63 row w sees, bit by bit (positions at or beyond the request's length
+// may be set too: they have no slot).
+__device__ __forceinline__ uint64_t sees64(const AttnArgs& a, const Row& w, const Request& q, int32_t j0) {
+  uint64_t bits = bits_below(w.hi - j0) & ~bits_below(w.lo - j0);
+  if (a.tree && w.token >= 0 && j0 + 64 > q.ctx) {
+    // the row's mask bits from drafted token d on, d = j0 - ctx > -64
+    const int64_t* words = a.tree + (int64_t)w.token * a.tree_ld;
+    const int32_t d = j0 - q.ctx;
+    if (d < 0) {
+      bits |= (uint64_t)words[0] << -d;
+    } else if ((d >> 6) < a.tree_words) {
+      bits |= (uint64_t)words[d >> 6] >> (d & 63);
+      if ((d & 63) && (d >> 6) + 1 < a.tree_words) bits |= (uint64_t)words[(d >> 6) + 1] << (64 - (d & 63));
+    }
+  }
+  return bits;
+}
+
+// x where bit b of `seen` is set, else -inf.  (In integer arithmetic: a tile's selections by condition
+// would hold as many lane masks in scalar registers.)
+__device__ __forceinline__ float kept(float x, uint32_t seen, int b) {
+  const uint32_t m = (uint32_t)((int32_t)(seen << (31 - b)) >> 31);
+  return __uint_as_float((__float_as_uint(x) & m) | (~m & 0xFF800000u));
 }
 
 // Position at which key j counts in the distance bias.
@@ -142,6 +163,9 @@ __device__ __forceinline__ int32_t slot_at(const AttnArgs& a, const int32_t* tab
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
 }
+
+// The four codes with NaN replaced by 0.
+__device__ __forceinline__ uint32_t without_nans(uint32_t w) { return w & ~((nan_codes(w) >> 7) * 0xFFu); }
 
 // 4 x 4 byte transpose: out[t] holds byte t of in[0 .. 3].
 __device__ __forceinline__ void transpose4(const uint32_t in[4], uint32_t out[4]) {
