@@ -84,7 +84,7 @@ nvfp4_status check(const Call& c, bool* empty) {
   if (!table_fits(c.requests, c.table_width, c.table_ld)) return NVFP4_ESHAPE;
   if (c.block_size < 1 || c.block_size > kMaxBlockSize) return NVFP4_ESHAPE;
   if (c.num_slots < 0 || c.num_slots > kMaxI32 || (!*empty && c.num_slots < 1)) return NVFP4_ESHAPE;
-  if (c.cache_ld < c.kv_heads * c.head_dim || c.cache_ld > kMaxSpan ||
+  if (c.cache_ld < c.kv_heads * c.head_dim || c.cache_ld > kMaxI32 ||
       (c.num_slots > 0 && c.cache_ld > kMaxSpan / c.num_slots))
     return NVFP4_ESHAPE;
   if (!*empty) {

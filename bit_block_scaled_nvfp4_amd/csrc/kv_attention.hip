@@ -46,14 +46,14 @@ __device__ __forceinline__ void load_codes(const AttnArgs& a, int32_t slot, cons
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int32_t sk = __shfl(s, 16 * t + d16);
-    const uint8_t* p = kbase + (int64_t)sk * a.cache_ld + g * 16;
+    const uint8_t* p = row_at(kbase, sk, a) + g * 16;
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) c.k[t][j] = *reinterpret_cast<const u32x4*>(p + 64 * j);
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const int32_t sv = __shfl(s, 16 * (e >> 2) + 4 * g + (e & 3));
-    const uint8_t* p = vbase + (int64_t)sv * a.cache_ld + d16 * (D / 16);
+    const uint8_t* p = row_at(vbase, sv, a) + d16 * (D / 16);
     if constexpr (D == 256) {
       const u32x4 w = *reinterpret_cast<const u32x4*>(p);
       c.v[e][0] = w.x; c.v[e][1] = w.y; c.v[e][2] = w.z; c.v[e][3] = w.w;
@@ -134,11 +134,12 @@ __device__ __forceinline__ void step(const AttnArgs& a, const Request& rq, Codes
         for (int n = 0; n < NQ; ++n) x[t][n] *= mul * kLog2e;
     }
     if (a.slopes) {
+      const int32_t* positions = a.tree ? a.positions : nullptr;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int32_t kp = key_position(a, rq, j0 + 16 * t + 4 * g + i);
+          const int32_t kp = key_position(positions, rq, j0 + 16 * t + 4 * g + i);
 #pragma unroll
           for (int n = 0; n < NQ; ++n)
             x[t][n][i] = __builtin_fmaf(s.row[n].slope, (float)(kp - s.row[n].pos), x[t][n][i]);
@@ -152,10 +153,11 @@ __device__ __forceinline__ void step(const AttnArgs& a, const Request& rq, Codes
   }
   // bit 16 t + i of seen[n] >> 4 g: whether row n sees position 16 t + 4 g + i of the step
   uint32_t seen[NQ];
-  if (!whole) {
+  const bool tree = a.tree != nullptr;
+  if (rarely(!whole)) {
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      seen[n] = ((uint32_t)sees64(a, s.row[n], rq, j0) & (uint32_t)in_cache) >> (4 * g);
+      seen[n] = ((uint32_t)sees64(s.row[n].lo, s.row[n].hi, tree ? s.row[n].token : -1, rq.ctx, j0) & (uint32_t)in_cache) >> (4 * g);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -166,21 +168,25 @@ __device__ __forceinline__ void step(const AttnArgs& a, const Request& rq, Codes
   u32x4 p[NQ];
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
-    float top = x[0][n][0];
+    float e[8], sum;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) top = __builtin_fmaxf(top, x[i >> 2][n][i & 3]);
-    if (__any(top > s.m[n] + kSlack)) {
+    for (int i = 0; i < 8; ++i) e[i] = exp2_of(x[i >> 2][n][i & 3] - s.m[n]);
+    sum = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+    if (rarely(__any(sum > kRaise))) {
+      float top = x[0][n][0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) top = __builtin_fmaxf(top, x[i >> 2][n][i & 3]);
       const float m = __builtin_fmaxf(s.m[n], max_over_groups(top));
       const float f = exp2_of(s.m[n] - m);
       s.m[n] = m;
       s.l[n] *= f;
 #pragma unroll
       for (int t = 0; t < D / 16; ++t) s.acc[n][t] *= f;
-    }
-    float e[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = exp2_of(x[i >> 2][n][i & 3] - s.m[n]);
-    s.l[n] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+      for (int i = 0; i < 8; ++i) e[i] = exp2_of(x[i >> 2][n][i & 3] - m);
+      sum = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+    }
+    s.l[n] += sum;
     p[n] = u32x4{pack_f16(e[0], e[1]), pack_f16(e[2], e[3]), pack_f16(e[4], e[5]), pack_f16(e[6], e[7])};
   }
 
@@ -188,7 +194,7 @@ __device__ __forceinline__ void step(const AttnArgs& a, const Request& rq, Codes
   // see must reach those rows alone, which a product with 0 would not give: it counts as 0 here too
   // and the rows that see it are set to NaN afterwards.
   bool nans = false;
-  if (!whole) {
+  if (rarely(!whole)) {
     uint32_t bad = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -200,7 +206,7 @@ __device__ __forceinline__ void step(const AttnArgs& a, const Request& rq, Codes
       }
     }
     nans = __any(bad != 0);
-    if (nans) {
+    if (rarely(nans)) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
 #pragma unroll
@@ -225,16 +231,16 @@ __device__ __forceinline__ void step(const AttnArgs& a, const Request& rq, Codes
       for (int n = 0; n < NQ; ++n) s.acc[n][4 * d + b] = mfma16<false>(w, p[n], s.acc[n][4 * d + b]);
     }
   }
-  if (nans) {
+  if (rarely(nans)) {
 #pragma unroll 1
     for (int o = 0; o < kStep; ++o) {
       const int32_t at = __shfl(slot, o);
       if (at < 0) continue;
       // this lane's dims are the D / 4 from g * D / 4 on
-      const uint8_t* p8 = vbase + (int64_t)at * a.cache_ld + g * (D / 4);
+      const uint8_t* p8 = row_at(vbase, at, a) + g * (D / 4);
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
-        const bool see = ((uint32_t)sees64(a, s.row[n], rq, j0) >> o) & 1;
+        const bool see = ((uint32_t)sees64(s.row[n].lo, s.row[n].hi, tree ? s.row[n].token : -1, rq.ctx, j0) >> o) & 1;
 #pragma unroll
         for (int w = 0; w < D / 16; ++w) {
           const uint32_t bad = see ? nan_codes(*reinterpret_cast<const uint32_t*>(p8 + 4 * w)) : 0u;
@@ -251,7 +257,8 @@ __device__ __forceinline__ void step(const AttnArgs& a, const Request& rq, Codes
 }
 
 template <int D, bool BF16, int NQ>
-__device__ __forceinline__ void segment(const AttnArgs& a, const Segment& sg, bool split, float* lds) {
+__device__ __forceinline__ void segment(const Segment& sg, bool split, float* lds) {
+  const AttnArgs& a = args();
   constexpr int kRows = 16 * NQ;
   constexpr int kPitch = D + 4;  // floats; 16 bytes a row apart, so a store's 8 lanes differ in banks
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -305,27 +312,31 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Segment& sg, bo
   const int32_t* table_row = a.table + (int64_t)sg.r * a.table_ld;
   const uint8_t* kbase = a.kc + (int64_t)sg.kv_head * D;
   const uint8_t* vbase = a.vc + (int64_t)sg.kv_head * D;
-  const int32_t off = wave * kStep + (lane & 31);
+  const uint32_t off = wave * kStep + (lane & 31);
+  // slots of step u from the table entries e loaded before; entries of a step past the last are
+  // loaded too (of some position) and not used
+  const auto slots = [&](int32_t e, int32_t u) { return slot_of(a, e, hi_max, (uint32_t)u * kUnit + off); };
+  const auto entries = [&](int32_t u) { return entry_of(a, table_row, (uint32_t)u * kUnit + off); };
   if (u0 < u1) {
-    int32_t s0 = slot_at(a, table_row, hi_max, u0 * kUnit + off);
-    int32_t s1 = u0 + 1 < u1 ? slot_at(a, table_row, hi_max, (u0 + 1) * kUnit + off) : -1;
+    int32_t s0 = slots(entries(u0), u0), s1;
+    int32_t e1 = entries(u0 + 1);
     Codes<D> c0, c1;
     load_codes<D>(a, s0, kbase, vbase, lane, c0);
     for (int32_t u = u0; u < u1; u += 2) {
-      int32_t s2 = -1, s3 = -1;
+      s1 = slots(e1, u + 1);
       if (u + 1 < u1) load_codes<D>(a, s1, kbase, vbase, lane, c1);
-      if (u + 2 < u1) s2 = slot_at(a, table_row, hi_max, (u + 2) * kUnit + off);
+      const int32_t e2 = entries(u + 2);
       step<D, BF16, NQ>(a, rq, c0, s0, vbase, u * kUnit + wave * kStep, mul, inv_cap, lane, s);
       if (u + 1 >= u1) break;
-      if (u + 2 < u1) load_codes<D>(a, s2, kbase, vbase, lane, c0);
-      if (u + 3 < u1) s3 = slot_at(a, table_row, hi_max, (u + 3) * kUnit + off);
+      s0 = slots(e2, u + 2);
+      if (u + 2 < u1) load_codes<D>(a, s0, kbase, vbase, lane, c0);
+      e1 = entries(u + 3);
       step<D, BF16, NQ>(a, rq, c1, s1, vbase, (u + 1) * kUnit + wave * kStep, mul, inv_cap, lane, s);
-      s0 = s2;
-      s1 = s3;
     }
   }
 
   // join the wavefronts
+  const AttnArgs& ea = args();
   float* ml = lds + kWaves * 16 * kPitch;  // [wave][kRows][2]
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
@@ -335,7 +346,7 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Segment& sg, bo
       ml[(wave * kRows + 16 * n + d16) * 2 + 1] = l;
     }
   }
-  const float vs = *a.vs;
+  const float vs = *ea.vs;
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     __syncthreads();
@@ -371,18 +382,18 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Segment& sg, bo
       for (int i = 0; i < 4; ++i) o[t + i] = sum[i];
     }
     const uint32_t rr = (uint32_t)(sg.tile * kRows + 16 * n + row);
-    if (rr < (uint32_t)rq.count * a.group.d) {
+    if (rr < (uint32_t)rq.count * ea.group.d) {
       if (split && !(sg.first && sg.last)) {
         const int64_t at = part_slot(blockIdx.x, sg.first) * kRows + 16 * n + row;
-        float* op = a.part + at * D + part * (D / 16);
+        float* op = ea.part + at * D + part * (D / 16);
 #pragma unroll
         for (int t = 0; t < D / 16; t += 4) *reinterpret_cast<f32x4*>(op + t) = f32x4{o[t], o[t + 1], o[t + 2], o[t + 3]};
-        if (part == 0) *reinterpret_cast<f32x2*>(a.part_ml + 2 * at) = f32x2{mr, lr};
+        if (part == 0) *reinterpret_cast<f32x2*>(ea.part_ml + 2 * at) = f32x2{mr, lr};
       } else {
-        const int32_t i = (int32_t)div_of(rr, a.group);
-        const int32_t head = sg.kv_head * (int32_t)a.group.d + (int32_t)(rr - (uint32_t)i * a.group.d);
+        const int32_t i = (int32_t)div_of(rr, ea.group);
+        const int32_t head = sg.kv_head * (int32_t)ea.group.d + (int32_t)(rr - (uint32_t)i * ea.group.d);
         const float inv = lr == 0.0f ? 0.0f : vs / lr;
-        uint16_t* op = a.out + (int64_t)(rq.start + i) * a.out_ts + (int64_t)head * a.out_hs + part * (D / 16);
+        uint16_t* op = ea.out + (int64_t)(rq.start + i) * ea.out_ts + (int64_t)head * ea.out_hs + part * (D / 16);
 #pragma unroll
         for (int t = 0; t < D / 16; t += 4)
           *reinterpret_cast<u32x2*>(op + t) = u32x2{pack_out<BF16>(o[t] * inv, o[t + 1] * inv), pack_out<BF16>(o[t + 2] * inv, o[t + 3] * inv)};
@@ -393,32 +404,31 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Segment& sg, bo
 }
 
 template <int D, bool BF16, int NQ>
-__global__ void __launch_bounds__(kThreads) attention_stream_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kThreads) attention_stream_kernel(AttnArgs) {
   constexpr int kRows = 16 * NQ;
   __shared__ __align__(16) float lds[kWaves * 16 * (D + 4) + kWaves * kRows * 2];
-  if (a.workers == 0) {
-    Segment s;
+  __shared__ Share<kThreads> share;
+  Segment s;
+  if (args().workers == 0) {
+    const AttnArgs& a = args();
     s.kv_head = blockIdx.x;
     s.r = blockIdx.y;
     s.first = s.last = true;
     s.last_worker = 0;
     const Request q = request_of(a, s.r);
     s.u0 = 0;
-    s.u1 = (q.len + kUnit - 1) / kUnit;
+    s.u1 = (int32_t)(((uint32_t)q.len + kUnit - 1) / kUnit);
     const int32_t tiles = (int32_t)(((uint32_t)q.count * a.group.d + kRows - 1) / kRows);
-    for (s.tile = blockIdx.z; s.tile < tiles; s.tile += gridDim.z) segment<D, BF16, NQ>(a, s, false, lds);
+    for (s.tile = blockIdx.z; s.tile < tiles; s.tile += gridDim.z) segment<D, BF16, NQ>(s, false, lds);
     return;
   }
-  __shared__ uint64_t scratch[kThreads / 64 + 2];
-  Share<kThreads> share;
-  share.begin(a, kRows, kUnit, scratch);
-  Segment s;
-  Header h{0, 0, 0, -1};
-  while (share.next(a, s)) {
-    if (s.first && !s.last) h = Header{s.r, s.tile, s.kv_head, s.last_worker};
-    segment<D, BF16, NQ>(a, s, true, lds);
+  share.begin(kRows, kUnit);
+  int32_t* header = args().headers + 4 * blockIdx.x;
+  if (threadIdx.x == 0) *reinterpret_cast<Header*>(header) = Header{0, 0, 0, -1};
+  while (share.next(kRows, kUnit, s)) {
+    if (s.first && !s.last && threadIdx.x == 0) *reinterpret_cast<Header*>(header) = Header{s.r, s.tile, s.kv_head, s.last_worker};
+    segment<D, BF16, NQ>(s, true, lds);
   }
-  if (threadIdx.x == 0) *reinterpret_cast<Header*>(a.headers + 4 * blockIdx.x) = h;
 }
 
 // Joins the pieces of the items that were shared out: block (w, y) takes four rows of the item that

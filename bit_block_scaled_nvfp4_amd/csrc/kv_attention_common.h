@@ -8,9 +8,10 @@
 // of positions, aligned at position 0).
 //
 // All exponentials are base 2: scores are multiplied by log2(e) once.  The softmax keeps a reference
-// value m per row instead of the exact running maximum: m is raised (and what is accumulated so far
-// scaled down) only when a score exceeds it by more than kSlack, so exp2(x - m) stays below
-// 2^kSlack = 256, far inside FP16, and the accumulators are not rescaled on most tiles.
+// value m per row instead of the running maximum: m is one of the row's scores, and is raised to the
+// largest so far (scaling down what is accumulated) only when a lane's sum of exp2(x - m) over one
+// tile passes kRaise.  Below that every single term is below kRaise too, far inside FP16, no maximum
+// is formed and nothing is rescaled; on most tiles that is the case.
 #pragma once
 
 #include "attention_internal.h"
@@ -29,9 +30,9 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kSlack = 8.0f;
-// Reference of a row that has seen nothing: below every finite score that FP32 sums of real keys
-// reach, and finite, so that exp2(-inf - m) is 0 and not NaN.
+constexpr float kRaise = 4096.0f;
+// Reference of a row that has seen nothing: so far below every score that the first one seen raises it
+// (exp2 overflows to infinity), and finite, so that exp2(-inf - m) is 0 and not NaN.
 constexpr float kNoScore = -1e37f;
 
 __device__ __forceinline__ uint32_t div_of(uint32_t n, const FastDiv& f) {
@@ -39,6 +40,25 @@ __device__ __forceinline__ uint32_t div_of(uint32_t n, const FastDiv& f) {
 }
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The kernel's arguments (its only parameter).  They are read anew wherever this is called: held in
+// scalar registers from the kernel's entry to its end, the sixty of them do not fit, and what the
+// compiler spills of them costs the loops vector registers.
+__device__ __forceinline__ const AttnArgs& args() {
+  typedef const __attribute__((address_space(4))) AttnArgs* Ptr;
+  Ptr p = (Ptr)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const AttnArgs*)p;
+}
+
+// A condition that rarely holds: registers are kept for the other side.
+__device__ __forceinline__ bool rarely(bool x) { return __builtin_expect(x, 0); }
+
+__device__ __forceinline__ int32_t uniform(int32_t x) { return __builtin_amdgcn_readfirstlane(x); }
+
+__device__ __forceinline__ uint64_t uniform64(uint64_t x) {
+  return (uint64_t)(uint32_t)uniform((int32_t)(x >> 32)) << 32 | (uint32_t)uniform((int32_t)x);
+}
 
 // ---- which positions a row sees -------------------------------------------------------------
 
@@ -70,20 +90,27 @@ __device__ __forceinline__ Request request_of(const AttnArgs& a, int32_t r) {
   return q;
 }
 
+// Row of q that holds query row `row` of the request, or -1 past its rows; tokens * heads < 2^31.
+__device__ __forceinline__ int32_t token_of(const AttnArgs& a, const Request& q, uint32_t row) {
+  return row < (uint32_t)q.count * a.group.d ? q.start + (int32_t)div_of(row, a.group) : -1;
+}
+
+__device__ __forceinline__ int32_t head_of(const AttnArgs& a, const Request& q, int32_t kv_head, uint32_t row) {
+  return kv_head * (int32_t)a.group.d + (int32_t)(row - div_of(row, a.group) * a.group.d);
+}
+
 __device__ __forceinline__ Row row_of(const AttnArgs& a, int32_t r, const Request& q, int32_t kv_head,
                                       uint32_t row) {
   Row w;
   w.lo = 0;
   w.hi = 0;
   w.pos = 0;
-  w.token = -1;
+  w.token = token_of(a, q, row);
   w.head = 0;
   w.slope = 0.0f;
-  if (row >= (uint32_t)q.count * a.group.d) return w;  // tokens * heads < 2^31
-  const int32_t i = (int32_t)div_of(row, a.group);
-  w.token = q.start + i;
-  w.head = kv_head * (int32_t)a.group.d + (int32_t)(row - (uint32_t)i * a.group.d);
-  w.pos = q.ctx + i;
+  if (w.token < 0) return w;
+  w.head = head_of(a, q, kv_head, row);
+  w.pos = q.ctx + (w.token - q.start);
   if (a.slopes) w.slope = a.slopes[w.head] * kLog2e;
   if (a.tree) {
     w.hi = q.ctx > 0 ? q.ctx : 0;
@@ -108,14 +135,15 @@ __device__ __forceinline__ uint64_t bits_below(int32_t x) {
   return x <= 0 ? 0ull : (x >= 64 ? ~0ull : (1ull << x) - 1);
 }
 
-// Which of positions j0 .. j0 + 63 row w sees, bit by bit (positions at or beyond the request's length
-// may be set too: they have no slot).
-__device__ __forceinline__ uint64_t sees64(const AttnArgs& a, const Row& w, const Request& q, int32_t j0) {
-  uint64_t bits = bits_below(w.hi - j0) & ~bits_below(w.lo - j0);
-  if (a.tree && w.token >= 0 && j0 + 64 > q.ctx) {
+// Which of positions j0 .. j0 + 63 a row sees, bit by bit (positions at or beyond the request's length
+// may be set too: they have no slot).  `token`: of a row of a drafted tree, else -1.
+__device__ __forceinline__ uint64_t sees64(int32_t lo, int32_t hi, int32_t token, int32_t ctx, int32_t j0) {
+  uint64_t bits = bits_below(hi - j0) & ~bits_below(lo - j0);
+  if (token >= 0 && j0 + 64 > ctx) {
     // the row's mask bits from drafted token d on, d = j0 - ctx > -64
-    const int64_t* words = a.tree + (int64_t)w.token * a.tree_ld;
-    const int32_t d = j0 - q.ctx;
+    const AttnArgs& a = args();
+    const int64_t* words = a.tree + (int64_t)token * a.tree_ld;
+    const int32_t d = j0 - ctx;
     if (d < 0) {
       bits |= (uint64_t)words[0] << -d;
     } else if ((d >> 6) < a.tree_words) {
@@ -133,10 +161,10 @@ __device__ __forceinline__ float kept(float x, uint32_t seen, int b) {
   return __uint_as_float((__float_as_uint(x) & m) | (~m & 0xFF800000u));
 }
 
-// Position at which key j counts in the distance bias.
-__device__ __forceinline__ int32_t key_position(const AttnArgs& a, const Request& q, int32_t j) {
-  if (!a.tree || !a.positions || j < q.ctx || j >= q.len) return j;
-  return a.positions[q.start + (j - q.ctx)];
+// Position at which key j counts in the distance bias; positions: of the drafted tokens, or NULL.
+__device__ __forceinline__ int32_t key_position(const int32_t* positions, const Request& q, int32_t j) {
+  if (!positions || j < q.ctx || j >= q.len) return j;
+  return positions[q.start + (j - q.ctx)];
 }
 
 // Score of a raw product x: capped and biased, in units of log2 (x is already times scale * key
@@ -148,15 +176,25 @@ __device__ __forceinline__ float capped(float x, float cap, float inv_cap) {
 
 // ---- cache rows -----------------------------------------------------------------------------
 
-// Slot of position j of request r, or -1 where it is not in the cache.  j may be any value.
-__device__ __forceinline__ int32_t slot_at(const AttnArgs& a, const int32_t* table_row, int32_t len,
-                                           int32_t j) {
-  if (j < 0 || j >= len) return -1;
-  const uint32_t col = div_of((uint32_t)j, a.bs);
-  if (col >= (uint32_t)a.table_width) return -1;
-  const int32_t b = table_row[col];
-  const int64_t s = (int64_t)b * a.bs.d + ((uint32_t)j - col * a.bs.d);
-  return (b >= 0 && s < a.num_slots) ? (int32_t)s : -1;
+// The block table's entry for position j (a position without one gets some other entry: slot_of masks
+// it).  Loaded a step before slot_of looks at it, so that nothing waits for the load.
+__device__ __forceinline__ int32_t entry_of(const AttnArgs& a, const int32_t* table_row, uint32_t j) {
+  if (a.table_width <= 0) return -1;
+  const uint32_t col = div_of(j, a.bs), last = (uint32_t)a.table_width - 1;
+  return table_row[col < last ? col : last];
+}
+
+// Slot of position j, or -1 where it is not in the cache or not below `end`.
+__device__ __forceinline__ int32_t slot_of(const AttnArgs& a, int32_t entry, int32_t end, uint32_t j) {
+  const uint32_t col = div_of(j, a.bs);
+  const int64_t s = (int64_t)entry * a.bs.d + (j - col * a.bs.d);
+  const bool there = j < (uint32_t)end && col < (uint32_t)a.table_width && entry >= 0 && s < a.num_slots;
+  return there ? (int32_t)s : -1;
+}
+
+// Address of a slot's row: cache_ld < 2^31.
+__device__ __forceinline__ const uint8_t* row_at(const uint8_t* base, int32_t slot, const AttnArgs& a) {
+  return base + (uint64_t)(uint32_t)slot * (uint32_t)a.cache_ld;
 }
 
 // Non-zero where one of the four codes is NaN (0x7F or 0xFF).
@@ -253,126 +291,154 @@ __device__ __forceinline__ uint64_t shfl_up64(uint64_t x, int d) {
   return (uint64_t)hi << 32 | lo;
 }
 
+// Quotient of 64-bit numbers that mostly fit 32 bits.
+__device__ __forceinline__ uint64_t quotient(uint64_t n, uint64_t d) {
+  return ((n | d) >> 32) == 0 ? (uint32_t)n / (uint32_t)d : n / d;
+}
+
 // The workers' shares: worker w takes units [W w / P, W (w + 1) / P) of the W units of all items, one
-// after another.  Every workgroup finds its own start by summing the requests' weights (two passes
-// over the lengths, NT requests at a time), with no launch before it and nothing kept.  scratch: 3 +
-// NT / 64 words of 64 bits in LDS.
+// after another.  Every workgroup finds its own start by summing the requests' weights (one pass over
+// the lengths, or two where there are more requests than threads), with no launch before it and
+// nothing kept.  The state lies in LDS and the first thread advances it: it is used once a segment.
 template <int NT>
 struct Share {
-  uint64_t W, x, end;    // all units; the next unit and the end of this worker's share
-  uint64_t base;         // units before request r
-  uint32_t units;        // of an item of request r
-  uint64_t total;        // of request r
-  int32_t r, rows, unit;
-  uint32_t P, w;
+  uint64_t W, x, end;  // all units; the next unit and the end of this worker's share
+  uint64_t base;       // units before request r
+  uint64_t total;      // of request r
+  uint64_t sums[NT / 64];
+  uint32_t units;      // of an item of request r
+  uint32_t P;
+  int32_t r;
+  int32_t more;
+  Segment segment;
 
-  __device__ __forceinline__ void begin(const AttnArgs& a, int32_t rows_, int32_t unit_, uint64_t* scratch) {
-    rows = rows_;
-    unit = unit_;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    constexpr int kW = NT / 64;
-    const int R = a.requests;
-    uint64_t sum = 0;
-    uint64_t mine = 0;  // inclusive sum up to this thread's request, where R <= NT
-    uint64_t own = 0;
-    for (int b = 0; b < R; b += NT) {
-      const int i = b + tid;
-      uint64_t t = 0;
-      uint32_t u = 0;
-      if (i < R) weight_of(a, i, rows, unit, u, t);
-      own = t;
+  // Sum over the wavefronts before this one, and over all; `t` becomes the wavefront's inclusive sum.
+  __device__ __forceinline__ void scan(uint64_t& t, uint64_t& before, uint64_t& all) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const uint64_t p = shfl_up64(t, d);
-        if (lane >= d) t += p;
-      }
-      if (lane == 63) scratch[wave] = t;
-      __syncthreads();
-      uint64_t before = sum;
-      for (int k = 0; k < kW; ++k) {
-        if (k < wave) before += scratch[k];
-        sum += scratch[k];
-      }
-      mine = before + t;
-      __syncthreads();
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint64_t p = shfl_up64(t, d);
+      if (lane >= d) t += p;
     }
-    W = sum;
-    // a worker takes two units at least: the smallest shares cost more to join than to compute
-    const uint64_t most = (W + 1) / 2;
-    P = (uint32_t)(most < (uint64_t)a.workers ? (most > 0 ? most : 1) : (uint64_t)a.workers);
-    w = blockIdx.x;
-    if (w >= P) {
-      x = end = 0;
-      return;
+    if (lane == 63) sums[wave] = t;
+    __syncthreads();
+    before = all = 0;
+    for (int k = 0; k < NT / 64; ++k) {
+      if (k < wave) before += sums[k];
+      all += sums[k];
     }
-    x = W * w / P;
-    end = W * (w + 1) / P;
-    if (x >= end) return;
-    // the request that holds unit x
-    if (R <= NT) {
-      if (tid < R && mine > x && mine - own <= x) {
-        scratch[kW] = mine - own;
-        scratch[kW + 1] = (uint64_t)tid;
-      }
-      __syncthreads();
-    } else {
-      uint64_t s = 0;
-      for (int b = 0; b < R; b += NT) {
-        const int i = b + tid;
-        uint64_t t = 0;
-        uint32_t u = 0;
-        if (i < R) weight_of(a, i, rows, unit, u, t);
-        const uint64_t o = t;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-          const uint64_t p = shfl_up64(t, d);
-          if (lane >= d) t += p;
-        }
-        if (lane == 63) scratch[wave] = t;
-        __syncthreads();
-        uint64_t before = s;
-        for (int k = 0; k < kW; ++k) {
-          if (k < wave) before += scratch[k];
-          s += scratch[k];
-        }
-        const uint64_t incl = before + t;
-        if (i < R && incl > x && incl - o <= x) {
-          scratch[kW] = incl - o;
-          scratch[kW + 1] = (uint64_t)i;
-        }
-        __syncthreads();
-        if (s > x) break;  // uniform: s is the same in every thread
-      }
-    }
-    base = scratch[kW];
-    r = (int32_t)scratch[kW + 1];
-    weight_of(a, r, rows, unit, units, total);
+    __syncthreads();
   }
 
-  // The next segment, or false when the share is done.  Uniform over the workgroup.
-  __device__ __forceinline__ bool next(const AttnArgs& a, Segment& s) {
-    if (x >= end) return false;
-    while (x >= base + total) {  // ends before r leaves the requests: x < W = the sum of all totals
-      base += total;
-      ++r;
-      weight_of(a, r, rows, unit, units, total);
+  __device__ __forceinline__ void begin(int32_t rows, int32_t unit) {
+    const AttnArgs& a = args();
+    const int tid = threadIdx.x;
+    const int R = a.requests;
+    uint64_t sum = 0, first = 0, mine = 0, own = 0;
+    for (int b = 0; b < R; b += NT) {
+      const int i = b + tid;
+      uint64_t t = 0, before, all;
+      uint32_t u;
+      if (i < R) weight_of(a, i, rows, unit, u, t);
+      own = t;
+      scan(t, before, all);
+      first = sum + before + t - own;  // of the last pass: used only where it is the first too
+      mine = own;
+      sum += all;
     }
-    const uint64_t y = x - base;
-    const uint64_t item = y / units;
-    const uint32_t off = (uint32_t)(y - item * units);
-    uint64_t n = units - off;
-    if (n > end - x) n = end - x;
-    s.r = r;
-    s.tile = (int32_t)(item / (uint32_t)a.kv_heads);
-    s.kv_head = (int32_t)(item - (uint64_t)s.tile * (uint32_t)a.kv_heads);
-    s.u0 = (int32_t)off;
-    s.u1 = (int32_t)(off + n);
-    s.first = off == 0;
-    s.last = off + n == units;
-    const uint64_t tail = base + (item + 1) * units;  // one past the item's last unit
-    // worker of unit tail - 1: the largest w with W w / P <= tail - 1, that is W w < tail P
-    s.last_worker = (int32_t)((tail * P - 1) / W);
-    x += n;
+    // a worker takes two units at least: smaller shares cost more to join than to compute
+    const uint64_t most = (sum + 1) / 2, limit = (uint64_t)a.workers;
+    const uint32_t p = (uint32_t)(most < limit ? (most > 0 ? most : 1) : limit);
+    const uint32_t w = blockIdx.x;
+    const uint64_t x0 = w < p ? quotient(sum * w, p) : 0, x1 = w < p ? quotient(sum * (w + 1), p) : 0;
+    if (tid == 0) {
+      W = sum;
+      P = p;
+      x = x0;
+      end = x1;
+      r = 0;
+      base = 0;
+    }
+    __syncthreads();
+    if (x0 < x1) {
+      // the request that holds unit x0
+      if (R <= NT) {
+        if (tid < R && first <= x0 && x0 < first + mine) {
+          base = first;
+          r = tid;
+        }
+      } else {
+        uint64_t s = 0;
+        for (int b = 0; b < R && s <= x0; b += NT) {
+          const int i = b + tid;
+          uint64_t t = 0, before, all;
+          uint32_t u;
+          if (i < R) weight_of(a, i, rows, unit, u, t);
+          const uint64_t o = t;
+          scan(t, before, all);
+          const uint64_t f = s + before + t - o;
+          if (i < R && f <= x0 && x0 < f + o) {
+            base = f;
+            r = i;
+          }
+          s += all;
+        }
+      }
+      __syncthreads();
+      if (tid == 0) {
+        uint32_t u;
+        uint64_t t;
+        weight_of(a, r, rows, unit, u, t);
+        units = u;
+        total = t;
+      }
+    }
+  }
+
+  // The next segment, or false when the share is done.  Uniform over the workgroup, which has to pass
+  // a barrier between two calls.
+  __device__ __forceinline__ bool next(int32_t rows, int32_t unit, Segment& s) {
+    if (threadIdx.x == 0) {
+      more = x < end;
+      if (x < end) {
+        const AttnArgs& a = args();
+        while (x >= base + total) {  // ends before r leaves the requests: x < W, the sum of all totals
+          base += total;
+          ++r;
+          uint32_t u;
+          uint64_t t;
+          weight_of(a, r, rows, unit, u, t);
+          units = u;
+          total = t;
+        }
+        const uint64_t y = x - base;
+        const uint64_t item = quotient(y, units);
+        const uint32_t off = (uint32_t)(y - item * units);
+        uint64_t n = units - off;
+        if (n > end - x) n = end - x;
+        segment.r = r;
+        segment.tile = (int32_t)quotient(item, (uint64_t)a.kv_heads);
+        segment.kv_head = (int32_t)(item - (uint64_t)segment.tile * (uint32_t)a.kv_heads);
+        segment.u0 = (int32_t)off;
+        segment.u1 = (int32_t)(off + n);
+        segment.first = off == 0;
+        segment.last = off + n == units;
+        const uint64_t tail = base + (item + 1) * units;  // one past the item's last unit
+        // worker of unit tail - 1: the largest w with W w / P <= tail - 1, that is W w < tail P
+        segment.last_worker = (int32_t)quotient(tail * P - 1, W);
+        x += n;
+      }
+    }
+    __syncthreads();
+    if (!uniform(more)) return false;
+    s.r = uniform(segment.r);
+    s.tile = uniform(segment.tile);
+    s.kv_head = uniform(segment.kv_head);
+    s.u0 = uniform(segment.u0);
+    s.u1 = uniform(segment.u1);
+    s.first = uniform(segment.first);
+    s.last = uniform(segment.last);
+    s.last_worker = uniform(segment.last_worker);
     return true;
   }
 };

@@ -28,27 +28,34 @@ constexpr int kThreads = 512;
 constexpr int kWaves = 8;
 constexpr int kRows = 32 * kWaves;
 constexpr int kTileBytes = 16384;
+constexpr int kLookUp = 4;  // wavefronts 4 .. 7 look up slots in turn
 
 template <int D>
 constexpr int kKeys = 8192 / D;  // positions of a tile: 32, 64, 128
 
-// Byte offset of 16-byte granule `gr` of key `key` in a K tile [key][D].  The granule index is
-// scrambled by the key so that 8 lanes reading one granule of 8 keys touch 8 different bank groups.
+// LDS layouts.  A 16-byte access is served to lanes {4 k .. 4 k + 3} of both halves of a wavefront (or to
+// 8 neighbours) at a time, from 8 columns of 16 bytes; column numbers are scrambled so that such
+// lanes, reading one granule (lane half: two neighbouring ones) of 4 or 8 neighbouring keys or dims,
+// touch 8 different columns, and so do the stores.
+
+// Byte offset of granule `gr` (8 dims) of key `key` in a K tile [key][D].
 template <int D>
 __device__ __forceinline__ int k_offset(int key, int gr) {
-  return key * (2 * D) + ((gr ^ (key & 7)) << 4);
+  const int f = (key & 2) | ((key >> 2) & 1) | ((key & 1) << 2);
+  return key * (2 * D) + ((gr ^ f) << 4);
 }
 
-// Byte offset of granule `gr` (8 keys) of dim `dim` in a V^T tile [dim][keys].  Reads take one granule
-// of 8 consecutive dims, writes half granules of 4 dims that lie 4 apart: the scramble separates both.
+// Byte offset of granule `gr` (8 keys) of dim `dim` in a V^T tile [dim][keys].  Stores write half
+// granules: 4 dims that lie 4 apart, 4 quads of keys.
 template <int D>
 __device__ __forceinline__ int v_offset(int dim, int gr) {
+  const int d0 = dim & 1, d1 = (dim >> 1) & 1, d2 = (dim >> 2) & 1, d3 = (dim >> 3) & 1;
   if constexpr (D == 256) {
-    // rows of 64 bytes, two to a bank cycle
-    const int k = dim >> 1;
-    return (k << 7) + (((((dim & 1) << 2) | gr) ^ (k & 7)) << 4);
+    // rows of 64 bytes, two to the 8 columns
+    const int f = d2 | ((d1 ^ d2) << 1) | (d3 << 2);
+    return ((dim >> 1) << 7) + ((((d0 << 2) | gr) ^ f) << 4);
   } else {
-    const int f = (dim & 1) | ((dim >> 1) & 2) | (((dim << 1) ^ (dim >> 1)) & 4);
+    const int f = d2 | ((d0 ^ d2) << 1) | ((d1 ^ d3) << 2);
     return dim * (2 * kKeys<D>) + ((gr ^ f) << 4);
   }
 }
@@ -81,29 +88,25 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// Slots of a tile's positions: lane l holds position l (and 64 + l).
-template <int D>
-struct Slots {
-  int32_t s[D == 64 ? 2 : 1];
-};
-
-template <int D>
-__device__ __forceinline__ Slots<D> look_up(const AttnArgs& a, const int32_t* table_row, int32_t end, int32_t j0, int lane) {
-  Slots<D> r;
-  r.s[0] = slot_at(a, table_row, end, j0 + (lane & (kKeys<D> - 1)));
-  if constexpr (D == 64) r.s[1] = slot_at(a, table_row, end, j0 + 64 + lane);
-  return r;
-}
-
 // Which of a tile's positions are in the cache, bit per position.
+template <int D>
 struct There {
-  uint64_t lo, hi;  // hi: positions 64 .. 127, all ones in a shorter tile
-  __device__ __forceinline__ bool all() const { return (lo & hi) == ~0ull; }
+  uint64_t lo;
+  __device__ __forceinline__ bool all() const { return lo == ~0ull; }
+  __device__ __forceinline__ uint64_t half(int) const { return lo; }
 };
+template <>
+struct There<64> {
+  uint64_t lo, hi;  // hi: positions 64 .. 127
+  __device__ __forceinline__ bool all() const { return (lo & hi) == ~0ull; }
+  __device__ __forceinline__ uint64_t half(int n) const { return n ? hi : lo; }
+};
+
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
 // This thread's codes of a tile on their way from the cache to LDS.
 struct Fetched {
-  u32x4 k;        // 16 dims of one key
+  u32x2 k[2];     // 8 dims of one key, twice
   uint32_t v[4];  // 4 dims of 4 consecutive keys
 };
 
@@ -116,53 +119,50 @@ __device__ __forceinline__ int v_quad(int lane, int wave) { return (lane & 3) + 
 template <int D>
 __device__ __forceinline__ int v_dim(int lane, int wave) { return 4 * ((lane >> 2) + 16 * (wave / (kKeys<D> / 16))); }
 
+// Slots of a tile (`sl`, in LDS) and which of them are in the cache; the codes are requested.
 template <int D>
-__device__ __forceinline__ void fetch(const AttnArgs& a, const Slots<D>& sl, const uint8_t* kbase, const uint8_t* vbase,
-                                      int tid, Fetched& f, There& there) {
+__device__ __forceinline__ void fetch(const AttnArgs& a, const int32_t* sl, const uint64_t* in_cache, const uint8_t* kbase,
+                                      const uint8_t* vbase, int tid, Fetched& f, There<D>& there) {
   const int lane = tid & 63, wave = tid >> 6;
-  there.lo = __ballot(sl.s[0] >= 0);
-  there.hi = ~0ull;
-  if constexpr (D == 64) there.hi = __ballot(sl.s[1] >= 0);
-  const int kk = k_key<D>(tid), q4 = 4 * v_quad<D>(lane, wave);
-  // the halves of a 128-position tile are uniform over a wavefront
-  int32_t from_k = sl.s[0], from_v = sl.s[0];
-  if constexpr (D == 64) {
-    from_k = wave >= 4 ? sl.s[1] : sl.s[0];
-    from_v = (wave & 7) >= 4 ? sl.s[1] : sl.s[0];
-  }
-  const int32_t sk = __shfl(from_k, kk & 63);
   // a position that is not in the cache reads slot 0 (there is one): its scores are masked, its values
   // replaced by zeros
-  f.k = *reinterpret_cast<const u32x4*>(kbase + (int64_t)(sk < 0 ? 0 : sk) * a.cache_ld + 16 * k_chunk<D>(tid));
+  const int32_t sk = max(sl[k_key<D>(tid)], 0);
+  const i32x4 sv = *reinterpret_cast<const i32x4*>(sl + 4 * v_quad<D>(lane, wave));
+  there.lo = uniform64(in_cache[0]);
+  if constexpr (D == 64) there.hi = uniform64(in_cache[1]);
+  const uint8_t* kp = row_at(kbase, sk, a) + 8 * k_chunk<D>(tid);
+  f.k[0] = *reinterpret_cast<const u32x2*>(kp);
+  f.k[1] = *reinterpret_cast<const u32x2*>(kp + D / 2);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int32_t sv = __shfl(from_v, (q4 + i) & 63);
-    f.v[i] = *reinterpret_cast<const uint32_t*>(vbase + (int64_t)(sv < 0 ? 0 : sv) * a.cache_ld + v_dim<D>(lane, wave));
-  }
+  for (int i = 0; i < 4; ++i) f.v[i] = *reinterpret_cast<const uint32_t*>(row_at(vbase, max(sv[i], 0), a) + v_dim<D>(lane, wave));
 }
 
-// Decode into LDS, values that are NaN as zeros; returns whether this wavefront's values hold one.
+// Decode into LDS.  `whole`: every row of the workgroup sees every position of the tile; else values
+// of positions that are not in the cache, and NaN codes, are staged as zeros.  Returns whether this
+// wavefront's values held such a code.
 template <int D, bool BF16>
-__device__ __forceinline__ bool stage(const Fetched& f, const There& there, char* kt, char* vt, int tid) {
+__device__ __forceinline__ bool stage(const Fetched& f, const There<D>& there, bool whole, char* kt, char* vt, int tid) {
   const int lane = tid & 63, wave = tid >> 6;
   const int kk = k_key<D>(tid), c = k_chunk<D>(tid);
-  const u32x2 k0 = decode_key<BF16>(f.k.x), k1 = decode_key<BF16>(f.k.y), k2 = decode_key<BF16>(f.k.z), k3 = decode_key<BF16>(f.k.w);
-  *reinterpret_cast<u32x4*>(kt + k_offset<D>(kk, 2 * c)) = u32x4{k0.x, k0.y, k1.x, k1.y};
-  *reinterpret_cast<u32x4*>(kt + k_offset<D>(kk, 2 * c + 1)) = u32x4{k2.x, k2.y, k3.x, k3.y};
-  const int quad = v_quad<D>(lane, wave), dim = v_dim<D>(lane, wave);
-  uint64_t from = there.lo;
-  if constexpr (D == 64) from = (wave & 7) >= 4 ? there.hi : there.lo;
-  const uint32_t four = (uint32_t)(from >> ((4 * quad) & 63));
-  uint32_t in[4], t[4], bad = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    in[i] = (four >> i) & 1 ? f.v[i] : 0u;
-    bad |= nan_codes(in[i]);
+  for (int e = 0; e < 2; ++e) {
+    const u32x2 lo = decode_key<BF16>(f.k[e].x), hi = decode_key<BF16>(f.k[e].y);
+    *reinterpret_cast<u32x4*>(kt + k_offset<D>(kk, c + e * (D / 16))) = u32x4{lo.x, lo.y, hi.x, hi.y};
   }
-  const bool any = __any(bad != 0);
-  if (any) {
+  const int quad = v_quad<D>(lane, wave), dim = v_dim<D>(lane, wave);
+  uint32_t in[4] = {f.v[0], f.v[1], f.v[2], f.v[3]}, t[4];
+  bool any = false;
+  if (rarely(!whole)) {
+    const uint64_t from = there.half(wave >= 4);
+    const uint32_t four = (uint32_t)(from >> ((4 * quad) & 63));
+    uint32_t bad = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) in[i] = without_nans(in[i]);
+    for (int i = 0; i < 4; ++i) {
+      in[i] = (four >> i) & 1 ? in[i] : 0u;
+      bad |= nan_codes(in[i]);
+      in[i] = without_nans(in[i]);
+    }
+    any = __any(bad != 0);
   }
   transpose4(in, t);
   // keys 16 s + 8 e + 4 h + i are half e of granule 2 s + h
@@ -172,18 +172,50 @@ __device__ __forceinline__ bool stage(const Fetched& f, const There& there, char
   return any;
 }
 
+// Score of element i of x[n], less m: x cm + (slope * offset + (bias - m)).
+template <bool MODS>
+__device__ __forceinline__ float score(float x, float cm, float slope, float shift, int n, int i) {
+  if constexpr (MODS) shift = __builtin_fmaf(slope, (float)(32 * n + 8 * (i >> 2) + (i & 3)), shift);
+  return __builtin_fmaf(x, cm, shift);
+}
+
+// exp2 of the scores less m in FP16, in the output product's operand layout; returns their sum in FP32.
+template <int N, bool MODS>
+__device__ __forceinline__ float exponentials(const f32x16 (&x)[N], float cm, float slope, float shift, u32x4 (&p)[2 * N]) {
+  float sum = 0.0f;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = exp2_of(score<MODS>(x[n][8 * u + i], cm, slope, shift, n, 8 * u + i));
+      sum += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+      p[2 * n + u] = u32x4{pack_f16(e[0], e[1]), pack_f16(e[2], e[3]), pack_f16(e[4], e[5]), pack_f16(e[6], e[7])};
+    }
+  return sum;
+}
+
+// Query operands of a wavefront that stay in registers; with 256 dims they, the output and the scores
+// do not fit 256 registers together, and the other half is read from LDS (8 more operand reads a tile,
+// beside 32).
+template <int D>
+constexpr int kQueryRegs = D == 256 ? 8 : D / 16;
+
 template <int D>
 struct WaveState {
-  u32x4 q[D / 16];
+  u32x4 q[kQueryRegs<D>];
   f32x16 acc[D / 32];  // acc[.][4 j + i]: dim 32 . + 8 j + 4 h + i
   float m, l;
-  Row row;
+  int32_t lo, hi;  // of the lane's row, as in Row; the rest of it is formed again where it is needed
+  int32_t pos;
+  float slope;
   int32_t lo_min, hi_max, lo_all, hi_all;  // over the wavefront's rows
 };
 
-template <int D, bool BF16>
-__device__ __forceinline__ void multiply(const AttnArgs& a, const Request& rq, const char* kt, const char* vt, const There& there,
-                                         bool nans, const int32_t* table_row, const uint8_t* vbase, int32_t j0, float c, float inv_cap, int lane, WaveState<D>& s) {
+template <int D, bool BF16, bool MODS>
+__device__ __forceinline__ void multiply(float cap, const Request& rq, const char* qt, const char* kt, const char* vt, const There<D>& there,
+                                         bool nans, bool moved, float* away, const Segment& now, uint32_t my_row, int32_t j0, float c, float inv_cap, int lane, WaveState<D>& s) {
   constexpr int N = kKeys<D> / 32;
   const int r = lane & 31, h = lane >> 5;
   const char *kp[4], *vp[4];
@@ -199,36 +231,53 @@ __device__ __forceinline__ void multiply(const AttnArgs& a, const Request& rq, c
     for (int i = 0; i < 16; ++i) x[n][i] = 0.0f;
 #pragma unroll
     for (int e = 0; e < D / 16; ++e)
-      x[n] = mfma32<BF16>(read_k<D>(kp, n, e), s.q[e], x[n]);
+      x[n] = mfma32<BF16>(read_k<D>(kp, n, e), e < kQueryRegs<D> ? s.q[e < kQueryRegs<D> ? e : 0] : *reinterpret_cast<const u32x4*>(qt + (e - kQueryRegs<D>) * 1024), x[n]);
   }
+  // the phases' instructions stay apart: mixed, they need more registers than there are
+  __builtin_amdgcn_sched_barrier(0);
   const bool whole = there.all() && j0 >= s.lo_all && j0 + kKeys<D> <= s.hi_all;
-  float cm = c;
-  if (a.cap > 0.0f || a.slopes || c == 0.0f) {
-    cm = 1.0f;
-    if (a.cap > 0.0f) {
+  // scores are x cm + bias, in units of log2; `bias` starts from the position's distance and each
+  // element adds its offset in the tile
+  float cm = c, bias = 0.0f;
+  if constexpr (MODS) {
+    if (cap > 0.0f) {
       const float mul = c * (1.0f / kLog2e);
 #pragma unroll
-      for (int n = 0; n < N; ++n)
+      for (int n = 0; n < N; ++n) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[n][i] = capped(x[n][i] * mul, a.cap, inv_cap) * kLog2e;
-    } else {
-#pragma unroll
-      for (int n = 0; n < N; ++n) x[n] *= c;
+        for (int i = 0; i < 16; ++i) x[n][i] = capped(x[n][i] * mul, cap, inv_cap);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      cm = kLog2e;
     }
-    if (a.slopes) {
+    bias = s.slope * (float)(j0 + 4 * h - s.pos);
+    if (rarely(moved && j0 + kKeys<D> > rq.ctx)) {
+      // drafted keys count at positions of their own: their difference from the place in the cache, by
+      // way of LDS (this wavefront's part)
+      const int32_t* positions = args().positions;
+#pragma unroll
+      for (int k = 0; k < kKeys<D>; k += 64) {
+        const int32_t j = j0 + k + lane;
+        if (k + lane < kKeys<D>) away[k + lane] = (float)(key_position(positions, rq, j) - j);
+      }
+      const float per = s.slope / cm;
 #pragma unroll
       for (int n = 0; n < N; ++n)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int32_t kp = key_position(a, rq, j0 + 32 * n + 8 * (i >> 2) + 4 * h + (i & 3));
-          x[n][i] = __builtin_fmaf(s.row.slope, (float)(kp - s.row.pos), x[n][i]);
+        for (int g = 0; g < 4; ++g) {
+          const f32x4 w = *reinterpret_cast<const f32x4*>(away + 32 * n + 8 * g + 4 * h);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[n][4 * g + i] = __builtin_fmaf(per, w[i], x[n][4 * g + i]);
+          __builtin_amdgcn_sched_barrier(0);
         }
     }
   }
-  if (!whole) {
+  if (rarely(!whole)) {
+    const AttnArgs& ra = args();
+    const int32_t token = ra.tree ? token_of(ra, rq, my_row) : -1;
 #pragma unroll
     for (int n2 = 0; n2 < N; n2 += 2) {
-      const uint64_t bits = sees64(a, s.row, rq, j0 + 32 * n2) & (n2 ? there.hi : there.lo);
+      const uint64_t bits = sees64(s.lo, s.hi, token, rq.ctx, j0 + 32 * n2) & there.half(n2);
       // bit 8 j + i: whether the row sees position 32 n + 8 j + 4 h + i
       const uint32_t seen0 = (uint32_t)bits >> (4 * h), seen1 = (uint32_t)(bits >> 32) >> (4 * h);
 #pragma unroll
@@ -238,46 +287,42 @@ __device__ __forceinline__ void multiply(const AttnArgs& a, const Request& rq, c
       }
     }
   }
-  float top = x[0][0];
+  u32x4 p[2 * N];
+  float sum = exponentials<N, MODS>(x, cm, s.slope, bias - s.m, p);
+  if (rarely(__any(sum > kRaise))) {
+    float top = score<MODS>(x[0][0], cm, s.slope, bias, 0, 0);
 #pragma unroll
-  for (int n = 0; n < N; ++n)
+    for (int n = 0; n < N; ++n)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, x[n][i]);
-  if (__any(top * cm > s.m + kSlack)) {
-    const float m = __builtin_fmaxf(s.m, other_half_max(top * cm));
+      for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, score<MODS>(x[n][i], cm, s.slope, bias, n, i));
+    const float m = __builtin_fmaxf(s.m, other_half_max(top));
     const float f = exp2_of(s.m - m);
     s.m = m;
     s.l *= f;
 #pragma unroll
     for (int d = 0; d < D / 32; ++d) s.acc[d] *= f;
+    sum = exponentials<N, MODS>(x, cm, s.slope, bias - m, p);
   }
-  u32x4 p[2 * N];
-  float sum = 0.0f;
-#pragma unroll
-  for (int n = 0; n < N; ++n)
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      float e[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = exp2_of(__builtin_fmaf(x[n][8 * u + i], cm, -s.m));
-      sum += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-      p[2 * n + u] = u32x4{pack_f16(e[0], e[1]), pack_f16(e[2], e[3]), pack_f16(e[4], e[5]), pack_f16(e[6], e[7])};
-    }
   s.l += sum;
+  __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int d = 0; d < D / 32; ++d)
 #pragma unroll
     for (int e = 0; e < 2 * N; ++e)
       s.acc[d] = mfma32<false>(read_v<D>(vp, d, e), p[e], s.acc[d]);
-  if (nans) {
+  if (rarely(nans)) {
     // NaN codes among the tile's values were staged as zeros, so that they cannot reach rows that do not
     // see them; the rows that do are set here, from the cache
+    const AttnArgs& ra = args();
+    const int32_t token = ra.tree ? token_of(ra, rq, my_row) : -1;
+    const int32_t request = uniform(now.r), kv_head = uniform(now.kv_head);
+    const int32_t* table_row = ra.table + (int64_t)request * ra.table_ld;
 #pragma unroll 1
     for (int o = 0; o < kKeys<D>; ++o) {
-      const int32_t at = slot_at(a, table_row, s.hi_max, j0 + o);
+      const int32_t at = slot_of(ra, entry_of(ra, table_row, j0 + o), s.hi_max, j0 + o);
       if (at < 0) continue;
-      const bool see = sees64(a, s.row, rq, j0 + o) & 1;
-      const uint8_t* p8 = vbase + (int64_t)at * a.cache_ld + 4 * h;
+      const bool see = sees64(s.lo, s.hi, token, rq.ctx, j0 + o) & 1;
+      const uint8_t* p8 = row_at(ra.vc + (int64_t)kv_head * D, at, ra) + 4 * h;
 #pragma unroll
       for (int d = 0; d < D / 32; ++d)
 #pragma unroll
@@ -291,17 +336,24 @@ __device__ __forceinline__ void multiply(const AttnArgs& a, const Request& rq, c
   }
 }
 
+template <int D>
 struct Shared {
   char tiles[2][2][kTileBytes];  // [buffer][K, V^T]
+  char query[D == 256 ? kWaves * 8192 : 16];  // [wavefront][operand][lane]
   int32_t limits[kWaves][4];
   int32_t nans[2][kWaves];
-  uint64_t scratch[kWaves + 2];
+  float away[kWaves][kKeys<D>];  // drafted keys' positions less their places
+  int32_t slots[4][128];    // of the tiles t with t % 4 = index
+  uint64_t in_cache[4][2];
+  Share<kThreads> share;
 };
 
-template <int D, bool BF16, bool SPLIT>
-__device__ __forceinline__ void segment(const AttnArgs& a, const Segment& sg, Shared& lds) {
+template <int D, bool BF16, bool MODS, bool SPLIT>
+__device__ __forceinline__ void segment(const Segment& sg, Shared<D>& lds) {
+  const AttnArgs& a = args();
   constexpr int BN = kKeys<D>;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int tid = threadIdx.x;
+  const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 31, h = lane >> 5;
   const Request rq = request_of(a, sg.r);
   WaveState<D> s;
@@ -309,26 +361,37 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Segment& sg, Sh
   // a negative factor goes into the query, so that the largest raw product is the largest score
   const uint32_t flip = c < 0.0f ? 0x80008000u : 0u;
   c = __builtin_fabsf(c);
+  // (and a factor of 0 too: -inf, a masked score, times 0 would be NaN)
+  const uint32_t keep = c == 0.0f ? 0u : 0xFFFFFFFFu;
+  if (c == 0.0f) c = 1.0f;
   const float inv_cap = a.cap > 0.0f ? 1.0f / a.cap : 0.0f;
+  const bool moved = MODS && a.tree && a.slopes && a.positions;
   const uint32_t my_row = (uint32_t)(sg.tile * kRows + 32 * wave + r);
-  s.row = row_of(a, sg.r, rq, sg.kv_head, my_row);
+  const Row row = row_of(a, sg.r, rq, sg.kv_head, my_row);
+  s.lo = row.lo;
+  s.hi = row.hi;
+  s.pos = row.pos;
+  s.slope = row.slope;
   s.m = kNoScore;
   s.l = 0.0f;
 #pragma unroll
   for (int d = 0; d < D / 32; ++d)
 #pragma unroll
     for (int i = 0; i < 16; ++i) s.acc[d][i] = 0.0f;
-  const uint16_t* qp = a.q + (int64_t)s.row.token * a.q_ts + (int64_t)s.row.head * a.q_hs + 8 * h;
+  const uint16_t* qp = a.q + (int64_t)row.token * a.q_ts + (int64_t)row.head * a.q_hs + 8 * h;
+  char* qt = lds.query + (D == 256 ? wave * 8192 + lane * 16 : 0);
 #pragma unroll
   for (int e = 0; e < D / 16; ++e) {
-    s.q[e] = u32x4{0, 0, 0, 0};
-    if (s.row.token >= 0) s.q[e] = *reinterpret_cast<const u32x4*>(qp + 16 * e) ^ flip;
+    u32x4 v = {0, 0, 0, 0};
+    if (row.token >= 0) v = (*reinterpret_cast<const u32x4*>(qp + 16 * e) ^ flip) & keep;
+    if (e < kQueryRegs<D>) s.q[e < kQueryRegs<D> ? e : 0] = v;
+    else *reinterpret_cast<u32x4*>(qt + (e - kQueryRegs<D>) * 1024) = v;  // read back by this lane only
   }
   int32_t lo_min = 0x7FFFFFFF, hi_max = 0, lo_all = 0, hi_all = 0x7FFFFFFF;
-  if (s.row.token >= 0) {
-    lo_min = lo_all = s.row.lo;
-    hi_max = a.tree ? rq.len : s.row.hi;
-    hi_all = s.row.hi;
+  if (row.token >= 0) {
+    lo_min = lo_all = row.lo;
+    hi_max = a.tree ? rq.len : row.hi;
+    hi_all = row.hi;
   }
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -344,15 +407,21 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Segment& sg, Sh
   if (lane == 0) {
     lds.limits[wave][0] = s.lo_min;
     lds.limits[wave][1] = s.hi_max;
+    lds.limits[wave][2] = s.lo_all;
+    lds.limits[wave][3] = s.hi_all;
   }
   __syncthreads();
-  lo_min = 0x7FFFFFFF;
-  hi_max = 0;
+  lo_min = hi_all = 0x7FFFFFFF;
+  hi_max = lo_all = 0;
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) {
     lo_min = min(lo_min, lds.limits[w][0]);
     hi_max = max(hi_max, lds.limits[w][1]);
+    lo_all = max(lo_all, lds.limits[w][2]);
+    hi_all = min(hi_all, lds.limits[w][3]);
   }
+  lo_all = __builtin_amdgcn_readfirstlane(lo_all);
+  hi_all = __builtin_amdgcn_readfirstlane(hi_all);
   lo_min = __builtin_amdgcn_readfirstlane(lo_min);
   hi_max = __builtin_amdgcn_readfirstlane(hi_max);
   int32_t t0 = sg.u0, t1 = sg.u1;
@@ -366,33 +435,65 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Segment& sg, Sh
   const int32_t* table_row = a.table + (int64_t)sg.r * a.table_ld;
   const uint8_t* kbase = a.kc + (int64_t)sg.kv_head * D;
   const uint8_t* vbase = a.vc + (int64_t)sg.kv_head * D;
+  // One wavefront looks up a tile's slots for all: the table entries are loaded in one turn, turned into
+  // slots in the next and used by everybody in the one after, two turns before the tile is multiplied.
+  const uint32_t o0 = lane & (BN - 1), o1 = 64 + lane;
+  int32_t e0 = 0, e1 = 0;
+  const auto load_entries = [&](int32_t t) {
+    e0 = entry_of(a, table_row, (uint32_t)t * BN + o0);
+    if constexpr (D == 64) e1 = entry_of(a, table_row, (uint32_t)t * BN + o1);
+  };
+  const auto put_slots = [&](int32_t t) {
+    const int32_t x = slot_of(a, e0, hi_max, (uint32_t)t * BN + o0);
+    const uint64_t b = __ballot(x >= 0);
+    if (lane < BN) lds.slots[t & 3][o0] = x;
+    uint64_t c1 = ~0ull;
+    if constexpr (D == 64) {
+      const int32_t y = slot_of(a, e1, hi_max, (uint32_t)t * BN + o1);
+      c1 = __ballot(y >= 0);
+      lds.slots[t & 3][o1] = y;
+    }
+    if (lane == 0) {
+      lds.in_cache[t & 3][0] = b;
+      lds.in_cache[t & 3][1] = c1;
+    }
+  };
   if (t0 < t1) {
     Fetched f;
-    There cur, nxt;
-    Slots<D> sl = look_up<D>(a, table_row, hi_max, t0 * BN, lane);
-    fetch<D>(a, sl, kbase, vbase, tid, f, cur);
-    sl = look_up<D>(a, table_row, hi_max, (t0 + 1) * BN, lane);
-    const bool bad = stage<D, BF16>(f, cur, lds.tiles[0][0], lds.tiles[0][1], tid);
+    There<D> cur, nxt;
+    // whether every row of the workgroup sees all of tile t
+    const auto whole = [&](int32_t t, const There<D>& th) { return th.all() && t * BN >= lo_all && (t + 1) * BN <= hi_all; };
+    // tiles t0 .. t0 + 2 by one wavefront each, and the first entries of the loop's own look-ups
+    load_entries(t0 + (wave < 3 ? wave : 3));
+    if (wave < 3) put_slots(t0 + wave);
+    lds_barrier();
+    fetch<D>(a, lds.slots[t0 & 3], lds.in_cache[t0 & 3], kbase, vbase, tid, f, cur);
+    const bool bad = stage<D, BF16>(f, cur, whole(t0, cur), lds.tiles[0][0], lds.tiles[0][1], tid);
     if (lane == 0) lds.nans[0][wave] = bad;
-    fetch<D>(a, sl, kbase, vbase, tid, f, nxt);
-    sl = look_up<D>(a, table_row, hi_max, (t0 + 2) * BN, lane);
+    fetch<D>(a, lds.slots[(t0 + 1) & 3], lds.in_cache[(t0 + 1) & 3], kbase, vbase, tid, f, nxt);
     lds_barrier();
     for (int32_t t = t0; t < t1; ++t) {
       const int b = (t - t0) & 1;
-      There after = nxt;
+      // LDS and cache offsets are formed anew in each turn (a few instructions): kept in registers
+      // through the loop, they push operands out to scratch memory
+      if constexpr (D == 256) asm volatile("" : "+v"(tid));
+      There<D> after = nxt;
       if (t + 1 < t1) {
-        const bool bad2 = stage<D, BF16>(f, nxt, lds.tiles[b ^ 1][0], lds.tiles[b ^ 1][1], tid);
+        const bool bad2 = stage<D, BF16>(f, nxt, whole(t + 1, nxt), lds.tiles[b ^ 1][0], lds.tiles[b ^ 1][1], tid);
         if (lane == 0) lds.nans[b ^ 1][wave] = bad2;
+        if (wave == kLookUp + (t & 3)) put_slots(t + 3);
         // positions past the last tile have no slot; they read slot 0 and are not used
-        fetch<D>(a, sl, kbase, vbase, tid, f, after);
-        sl = look_up<D>(a, table_row, hi_max, (t + 3) * BN, lane);
+        fetch<D>(a, lds.slots[(t + 2) & 3], lds.in_cache[(t + 2) & 3], kbase, vbase, tid, f, after);
+        if (wave == kLookUp + ((t + 1) & 3)) load_entries(t + 4);
       }
       const int32_t j0 = t * BN;
       if (j0 < s.hi_max && j0 + BN > s.lo_min) {
         int32_t nans = 0;
+        if (rarely(!whole(t, cur))) {
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) nans |= lds.nans[b][w];
-        multiply<D, BF16>(a, rq, lds.tiles[b][0], lds.tiles[b][1], cur, __builtin_amdgcn_readfirstlane(nans) != 0, table_row, vbase, j0, c, inv_cap, lane, s);
+          for (int w = 0; w < kWaves; ++w) nans |= lds.nans[b][w];
+        }
+        multiply<D, BF16, MODS>(a.cap, rq, qt, lds.tiles[b][0], lds.tiles[b][1], cur, uniform(nans) != 0, moved, lds.away[wave], lds.share.segment, my_row, j0, c, inv_cap, lane, s);
       }
       cur = nxt;
       nxt = after;
@@ -401,19 +502,24 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Segment& sg, Sh
   }
 
   const float l = s.l + __shfl_xor(s.l, 32);
-  if (s.row.token >= 0) {
-    if (SPLIT && !(sg.first && sg.last)) {
-      const int64_t at = part_slot(blockIdx.x, sg.first) * kRows + 32 * wave + r;
-      float* op = a.part + at * D + 4 * h;
+  const AttnArgs& ea = args();
+  const int32_t token = token_of(ea, rq, my_row);
+  if (token >= 0) {
+    const Segment& now = lds.share.segment;
+    const bool first = uniform(now.first), last = uniform(now.last);
+    if (SPLIT && !(first && last)) {
+      const int64_t at = part_slot(blockIdx.x, first) * kRows + 32 * wave + r;
+      float* op = ea.part + at * D + 4 * h;
 #pragma unroll
       for (int d = 0; d < D / 32; ++d)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           *reinterpret_cast<f32x4*>(op + 32 * d + 8 * j) = f32x4{s.acc[d][4 * j], s.acc[d][4 * j + 1], s.acc[d][4 * j + 2], s.acc[d][4 * j + 3]};
-      if (h == 0) *reinterpret_cast<f32x2*>(a.part_ml + 2 * at) = f32x2{s.m, l};
+      if (h == 0) *reinterpret_cast<f32x2*>(ea.part_ml + 2 * at) = f32x2{s.m, l};
     } else {
-      const float inv = l == 0.0f ? 0.0f : *a.vs / l;
-      uint16_t* op = a.out + (int64_t)s.row.token * a.out_ts + (int64_t)s.row.head * a.out_hs + 4 * h;
+      const float inv = l == 0.0f ? 0.0f : *ea.vs / l;
+      const int32_t head = head_of(ea, rq, uniform(lds.share.segment.kv_head), my_row);
+      uint16_t* op = ea.out + (int64_t)token * ea.out_ts + (int64_t)head * ea.out_hs + 4 * h;
 #pragma unroll
       for (int d = 0; d < D / 32; ++d)
 #pragma unroll
@@ -425,54 +531,56 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Segment& sg, Sh
   __syncthreads();  // the next segment writes the limits and the tiles again
 }
 
-// SPLIT: the workgroups share the items' keys; else each takes whole items.
-template <int D, bool BF16, bool SPLIT>
-__global__ void __launch_bounds__(kThreads) attention_tiled_kernel(AttnArgs a) {
-  __shared__ __align__(16) Shared lds;
+// MODS: scores are capped or biased.  SPLIT: the workgroups share the items' keys; else each takes whole items.
+template <int D, bool BF16, bool MODS, bool SPLIT>
+__global__ void __launch_bounds__(kThreads) attention_tiled_kernel(AttnArgs) {
+  __shared__ __align__(16) Shared<D> lds;
+  Segment s;
   if constexpr (!SPLIT) {
-    Segment s;
+    const AttnArgs& a = args();
     s.kv_head = blockIdx.x;
     s.r = blockIdx.y;
     s.first = s.last = true;
     s.last_worker = 0;
     const Request q = request_of(a, s.r);
     s.u0 = 0;
-    s.u1 = (q.len + kKeys<D> - 1) / kKeys<D>;
+    s.u1 = (int32_t)(((uint32_t)q.len + kKeys<D> - 1) / kKeys<D>);
     const int32_t tiles = (int32_t)(((uint32_t)q.count * a.group.d + kRows - 1) / kRows);
     // the last row tiles see the most keys: they start first
     for (int32_t k = blockIdx.z; k < tiles; k += gridDim.z) {
       s.tile = tiles - 1 - k;
-      segment<D, BF16, false>(a, s, lds);
+      if (threadIdx.x == 0) lds.share.segment = s;  // read again behind segment()'s first barrier
+      segment<D, BF16, MODS, false>(s, lds);
     }
   } else {
-    Share<kThreads> share;
-    share.begin(a, kRows, kKeys<D>, lds.scratch);
-    Segment s;
-    Header hd{0, 0, 0, -1};
-    while (share.next(a, s)) {
-      if (s.first && !s.last) hd = Header{s.r, s.tile, s.kv_head, s.last_worker};
-      segment<D, BF16, true>(a, s, lds);
+    lds.share.begin(kRows, kKeys<D>);
+    int32_t* header = args().headers + 4 * blockIdx.x;
+    if (threadIdx.x == 0) *reinterpret_cast<Header*>(header) = Header{0, 0, 0, -1};
+    while (lds.share.next(kRows, kKeys<D>, s)) {
+      if (s.first && !s.last && threadIdx.x == 0) *reinterpret_cast<Header*>(header) = Header{s.r, s.tile, s.kv_head, s.last_worker};
+      segment<D, BF16, MODS, true>(s, lds);
     }
-    if (threadIdx.x == 0) *reinterpret_cast<Header*>(a.headers + 4 * blockIdx.x) = hd;
   }
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool MODS>
 void launch(const AttnArgs& a, hipStream_t stream) {
   if (a.workers) {
-    hipLaunchKernelGGL((attention_tiled_kernel<D, BF16, true>), dim3((uint32_t)a.workers), dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL((attention_tiled_kernel<D, BF16, MODS, true>), dim3((uint32_t)a.workers), dim3(kThreads), 0, stream, a);
   } else {
     const dim3 grid((uint32_t)a.kv_heads, (uint32_t)a.requests, (uint32_t)a.row_tiles);
-    hipLaunchKernelGGL((attention_tiled_kernel<D, BF16, false>), grid, dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL((attention_tiled_kernel<D, BF16, MODS, false>), grid, dim3(kThreads), 0, stream, a);
   }
 }
 
 template <int D>
 void launch(const AttnArgs& a, bool bf16, hipStream_t stream) {
-  if (bf16)
-    launch<D, true>(a, stream);
-  else
-    launch<D, false>(a, stream);
+  const bool mods = a.cap > 0.0f || a.slopes;
+  if (bf16) {
+    if (mods) launch<D, true, true>(a, stream); else launch<D, true, false>(a, stream);
+  } else {
+    if (mods) launch<D, false, true>(a, stream); else launch<D, false, false>(a, stream);
+  }
 }
 
 }  // namespace

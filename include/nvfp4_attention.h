@@ -105,7 +105,7 @@ nvfp4_status nvfp4_kv_block_tables(const int32_t* context_lens, const int32_t* q
  *   heads, kv_heads  1 <= kv_heads <= heads <= 1024, heads a multiple of kv_heads.
  *   head_dim      64, 128 or 256.
  *   key_cache, value_cache, num_slots, cache_ld  as nvfp4_kv_fp8_store wrote them (16-byte aligned,
- *                 cache_ld a multiple of 16 and >= kv_heads * head_dim); 1 <= num_slots < 2^31.
+ *                 cache_ld a multiple of 16, >= kv_heads * head_dim and < 2^31); 1 <= num_slots < 2^31.
  *   key_scale, value_scale  device, one float each (decode direction).
  *   block_table   device, int32 [requests, table_width], row pitch table_ld.
  *   query_start, seq_lens   device, int32[requests + 1] (not decreasing) and int32[requests].
