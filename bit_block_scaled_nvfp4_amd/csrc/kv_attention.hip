@@ -30,6 +30,14 @@ constexpr int kWaves = 4;
 constexpr int kStep = 32;              // positions of a wavefront's step
 constexpr int kUnit = kWaves * kStep;  // positions of a workgroup's step
 
+// Workgroups that share a compute unit's registers: what a call is divided among.  More of them keep more
+// loads in flight, as long as their operands fit: 4 KB a step and wavefront with 64 dims, 16 KB with 256.
+constexpr int stream_groups(int head_dim, int rows) {
+  if (head_dim == 64) return rows == 16 ? 4 : (rows == 32 ? 2 : 1);
+  if (head_dim == 128) return rows <= 32 ? 2 : 1;
+  return 1;
+}
+
 // Codes of 32 positions as a lane holds them.
 template <int D>
 struct Codes {
@@ -116,40 +124,40 @@ __device__ __forceinline__ void step(const AttnArgs& a, const Request& rq, Codes
         for (int n = 0; n < NQ; ++n) x[t][n] = mfma16<BF16>(k, s.q[n][2 * j + h], x[t][n]);
       }
 
+  __builtin_amdgcn_sched_barrier(0);  // the phases' instructions stay apart, to keep their registers few
   // wave-uniform: every position of the step is in the cache and seen by every row of the tile
   const uint64_t in_cache = __ballot(slot >= 0);
   const bool whole = in_cache == ~0ull && j0 >= s.lo_all && j0 + kStep <= s.hi_all;
-  if (a.cap > 0.0f || a.slopes) {
-    if (a.cap > 0.0f) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[t][n][i] = capped(x[t][n][i] * mul, a.cap, inv_cap) * kLog2e;
-    } else {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) x[t][n] *= mul * kLog2e;
-    }
-    if (a.slopes) {
-      const int32_t* positions = a.tree ? a.positions : nullptr;
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int32_t kp = key_position(positions, rq, j0 + 16 * t + 4 * g + i);
-#pragma unroll
-          for (int n = 0; n < NQ; ++n)
-            x[t][n][i] = __builtin_fmaf(s.row[n].slope, (float)(kp - s.row[n].pos), x[t][n][i]);
-        }
-    }
-  } else {
+  // scores are x cm + base, in units of log2
+  float cm = mul * kLog2e, base = 0.0f;
+  if (a.cap > 0.0f) {
+    const float to_r = cm * inv_cap * 2.0f;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int n = 0; n < NQ; ++n) x[t][n] *= mul * kLog2e;
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[t][n][i] = cap_term(x[t][n][i], to_r);
+    base = a.cap * kLog2e;
+    cm = -2.0f * base;
+  }
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[t][n][i] = __builtin_fmaf(x[t][n][i], cm, base);
+  if (a.slopes) {
+    const int32_t* positions = a.tree ? a.positions : nullptr;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int32_t kp = key_position(positions, rq, j0 + 16 * t + 4 * g + i);
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+          x[t][n][i] = __builtin_fmaf(s.row[n].slope, (float)(kp - s.row[n].pos), x[t][n][i]);
+      }
   }
   // bit 16 t + i of seen[n] >> 4 g: whether row n sees position 16 t + 4 g + i of the step
   uint32_t seen[NQ];
@@ -161,7 +169,7 @@ __device__ __forceinline__ void step(const AttnArgs& a, const Request& rq, Codes
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[t][n][i] = kept(x[t][n][i], seen[n], 16 * t + i);
+        for (int i = 0; i < 4; ++i) x[t][n][i] = kept(x[t][n][i], seen[n], 16 * t + i, kMinusInf);
     }
   }
 
@@ -193,6 +201,7 @@ __device__ __forceinline__ void step(const AttnArgs& a, const Request& rq, Codes
   // Values of positions outside the cache count as zeros.  A NaN code in a position that only some rows
   // see must reach those rows alone, which a product with 0 would not give: it counts as 0 here too
   // and the rows that see it are set to NaN afterwards.
+  __builtin_amdgcn_sched_barrier(0);
   bool nans = false;
   if (rarely(!whole)) {
     uint32_t bad = 0;
@@ -313,25 +322,29 @@ __device__ __forceinline__ void segment(const Segment& sg, bool split, float* ld
   const uint8_t* kbase = a.kc + (int64_t)sg.kv_head * D;
   const uint8_t* vbase = a.vc + (int64_t)sg.kv_head * D;
   const uint32_t off = wave * kStep + (lane & 31);
-  // slots of step u from the table entries e loaded before; entries of a step past the last are
-  // loaded too (of some position) and not used
+  // slots of step u from the table entries e loaded before; entries of a unit before the
+  // first are loaded too (of some position) and not used
   const auto slots = [&](int32_t e, int32_t u) { return slot_of(a, e, hi_max, (uint32_t)u * kUnit + off); };
   const auto entries = [&](int32_t u) { return entry_of(a, table_row, (uint32_t)u * kUnit + off); };
+  // from the last unit to the first: what is nearest, and with a distance bias weighs most, comes first
+  // and sets the reference
   if (u0 < u1) {
-    int32_t s0 = slots(entries(u0), u0), s1;
-    int32_t e1 = entries(u0 + 1);
+    int32_t u = u1 - 1;
+    int32_t s0 = slots(entries(u), u), s1;
+    int32_t e1 = entries(u - 1);
     Codes<D> c0, c1;
     load_codes<D>(a, s0, kbase, vbase, lane, c0);
-    for (int32_t u = u0; u < u1; u += 2) {
-      s1 = slots(e1, u + 1);
-      if (u + 1 < u1) load_codes<D>(a, s1, kbase, vbase, lane, c1);
-      const int32_t e2 = entries(u + 2);
+    for (;; u -= 2) {
+      s1 = slots(e1, u - 1);
+      if (u > u0) load_codes<D>(a, s1, kbase, vbase, lane, c1);
+      const int32_t e2 = entries(u - 2);
       step<D, BF16, NQ>(a, rq, c0, s0, vbase, u * kUnit + wave * kStep, mul, inv_cap, lane, s);
-      if (u + 1 >= u1) break;
-      s0 = slots(e2, u + 2);
-      if (u + 2 < u1) load_codes<D>(a, s0, kbase, vbase, lane, c0);
-      e1 = entries(u + 3);
-      step<D, BF16, NQ>(a, rq, c1, s1, vbase, (u + 1) * kUnit + wave * kStep, mul, inv_cap, lane, s);
+      if (u - 1 < u0) break;
+      s0 = slots(e2, u - 2);
+      if (u - 1 > u0) load_codes<D>(a, s0, kbase, vbase, lane, c0);
+      e1 = entries(u - 3);
+      step<D, BF16, NQ>(a, rq, c1, s1, vbase, (u - 1) * kUnit + wave * kStep, mul, inv_cap, lane, s);
+      if (u - 2 < u0) break;
     }
   }
 
@@ -404,7 +417,7 @@ __device__ __forceinline__ void segment(const Segment& sg, bool split, float* ld
 }
 
 template <int D, bool BF16, int NQ>
-__global__ void __launch_bounds__(kThreads) attention_stream_kernel(AttnArgs) {
+__global__ void __launch_bounds__(kThreads, stream_groups(D, 16 * NQ)) attention_stream_kernel(AttnArgs) {
   constexpr int kRows = 16 * NQ;
   __shared__ __align__(16) float lds[kWaves * 16 * (D + 4) + kWaves * kRows * 2];
   __shared__ Share<kThreads> share;
@@ -533,7 +546,7 @@ AttnPlan plan_attention(int64_t heads, int64_t kv_heads, int64_t head_dim, int64
   if (p.kernel == AttnKernel::Tiled) {
     if (max_seq_len > 256 && items < kComputeUnits) p.workers = kComputeUnits;
   } else if (max_seq_len > 2 * kUnit && items < 4 * kComputeUnits) {
-    p.workers = 2 * kComputeUnits;
+    p.workers = stream_groups((int)head_dim, p.rows) * kComputeUnits;
   }
   if (p.workers)
     p.workspace = (int64_t)p.workers * (2 * (int64_t)p.rows * (head_dim + 2) + 4) * (int64_t)sizeof(float);

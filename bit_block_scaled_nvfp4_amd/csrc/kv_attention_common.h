@@ -154,11 +154,11 @@ __device__ __forceinline__ uint64_t sees64(int32_t lo, int32_t hi, int32_t token
   return bits;
 }
 
-// x where bit b of `seen` is set, else -inf.  (In integer arithmetic: a tile's selections by condition
+// x where bit b of `seen` is set, else the value with bits `none`, an infinity.  (In integer arithmetic: a tile's selections by condition
 // would hold as many lane masks in scalar registers.)
-__device__ __forceinline__ float kept(float x, uint32_t seen, int b) {
+__device__ __forceinline__ float kept(float x, uint32_t seen, int b, uint32_t none) {
   const uint32_t m = (uint32_t)((int32_t)(seen << (31 - b)) >> 31);
-  return __uint_as_float((__float_as_uint(x) & m) | (~m & 0xFF800000u));
+  return __uint_as_float((__float_as_uint(x) & m) | (~m & none));
 }
 
 // Position at which key j counts in the distance bias; positions: of the drafted tokens, or NULL.
@@ -167,11 +167,12 @@ __device__ __forceinline__ int32_t key_position(const int32_t* positions, const 
   return positions[q.start + (j - q.ctx)];
 }
 
-// Score of a raw product x: capped and biased, in units of log2 (x is already times scale * key
-// scale here).  tanh(y) = 1 - 2 / (exp(2 y) + 1): its error is a few 2^-24, times the cap.
-__device__ __forceinline__ float capped(float x, float cap, float inv_cap) {
-  const float e = exp2_of(x * inv_cap * (2.0f * kLog2e));
-  return __builtin_fmaf(-2.0f * cap, __builtin_amdgcn_rcpf(e + 1.0f), cap);
+// The cap in units of log2(e): cap tanh(y) log2(e) = L - 2 L r with L = cap log2(e) and
+// r = 1 / (exp(2 y) + 1).  This is r, for to_r = 2 log2(e) / cap times what turns x into a score; the
+// product with -2 L joins the scaling that every score goes through.  r is off by a few 2^-24, the
+// capped score by as much times 2 L.
+__device__ __forceinline__ float cap_term(float x, float to_r) {
+  return __builtin_amdgcn_rcpf(exp2_of(x * to_r) + 1.0f);
 }
 
 // ---- cache rows -----------------------------------------------------------------------------
@@ -300,6 +301,8 @@ __device__ __forceinline__ uint64_t quotient(uint64_t n, uint64_t d) {
 // after another.  Every workgroup finds its own start by summing the requests' weights (one pass over
 // the lengths, or two where there are more requests than threads), with no launch before it and
 // nothing kept.  The state lies in LDS and the first thread advances it: it is used once a segment.
+constexpr uint32_t kMinusInf = 0xFF800000u, kPlusInf = 0x7F800000u;
+
 template <int NT>
 struct Share {
   uint64_t W, x, end;  // all units; the next unit and the end of this worker's share

@@ -239,18 +239,22 @@ __device__ __forceinline__ void multiply(float cap, const Request& rq, const cha
   // scores are x cm + bias, in units of log2; `bias` starts from the position's distance and each
   // element adds its offset in the tile
   float cm = c, bias = 0.0f;
+  uint32_t none = kMinusInf;  // times cm: -inf
   if constexpr (MODS) {
+    float base = 0.0f;
     if (cap > 0.0f) {
-      const float mul = c * (1.0f / kLog2e);
+      const float to_r = c * inv_cap * 2.0f;
 #pragma unroll
       for (int n = 0; n < N; ++n) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[n][i] = capped(x[n][i] * mul, cap, inv_cap);
+        for (int i = 0; i < 16; ++i) x[n][i] = cap_term(x[n][i], to_r);
         __builtin_amdgcn_sched_barrier(0);
       }
-      cm = kLog2e;
+      base = cap * kLog2e;
+      cm = -2.0f * base;
+      none = kPlusInf;
     }
-    bias = s.slope * (float)(j0 + 4 * h - s.pos);
+    bias = __builtin_fmaf(s.slope, (float)(j0 + 4 * h - s.pos), base);
     if (rarely(moved && j0 + kKeys<D> > rq.ctx)) {
       // drafted keys count at positions of their own: their difference from the place in the cache, by
       // way of LDS (this wavefront's part)
@@ -282,8 +286,8 @@ __device__ __forceinline__ void multiply(float cap, const Request& rq, const cha
       const uint32_t seen0 = (uint32_t)bits >> (4 * h), seen1 = (uint32_t)(bits >> 32) >> (4 * h);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        x[n2][i] = kept(x[n2][i], seen0, 8 * (i >> 2) + (i & 3));
-        if constexpr (N > 1) x[n2 + 1][i] = kept(x[n2 + 1][i], seen1, 8 * (i >> 2) + (i & 3));
+        x[n2][i] = kept(x[n2][i], seen0, 8 * (i >> 2) + (i & 3), none);
+        if constexpr (N > 1) x[n2 + 1][i] = kept(x[n2 + 1][i], seen1, 8 * (i >> 2) + (i & 3), none);
       }
     }
   }
@@ -458,33 +462,36 @@ __device__ __forceinline__ void segment(const Segment& sg, Shared<D>& lds) {
       lds.in_cache[t & 3][1] = c1;
     }
   };
+  // from the last tile to the first: what is nearest, and with a distance bias weighs most, comes first
+  // and sets the reference
   if (t0 < t1) {
     Fetched f;
     There<D> cur, nxt;
     // whether every row of the workgroup sees all of tile t
     const auto whole = [&](int32_t t, const There<D>& th) { return th.all() && t * BN >= lo_all && (t + 1) * BN <= hi_all; };
-    // tiles t0 .. t0 + 2 by one wavefront each, and the first entries of the loop's own look-ups
-    load_entries(t0 + (wave < 3 ? wave : 3));
-    if (wave < 3) put_slots(t0 + wave);
+    // the first three tiles by one wavefront each, and the first entries of the loop's own look-ups
+    const int32_t te = t1 - 1;
+    load_entries(te - (wave < 3 ? wave : 3));
+    if (wave < 3) put_slots(te - wave);
     lds_barrier();
-    fetch<D>(a, lds.slots[t0 & 3], lds.in_cache[t0 & 3], kbase, vbase, tid, f, cur);
-    const bool bad = stage<D, BF16>(f, cur, whole(t0, cur), lds.tiles[0][0], lds.tiles[0][1], tid);
+    fetch<D>(a, lds.slots[te & 3], lds.in_cache[te & 3], kbase, vbase, tid, f, cur);
+    const bool bad = stage<D, BF16>(f, cur, whole(te, cur), lds.tiles[0][0], lds.tiles[0][1], tid);
     if (lane == 0) lds.nans[0][wave] = bad;
-    fetch<D>(a, lds.slots[(t0 + 1) & 3], lds.in_cache[(t0 + 1) & 3], kbase, vbase, tid, f, nxt);
+    fetch<D>(a, lds.slots[(te - 1) & 3], lds.in_cache[(te - 1) & 3], kbase, vbase, tid, f, nxt);
     lds_barrier();
-    for (int32_t t = t0; t < t1; ++t) {
-      const int b = (t - t0) & 1;
+    for (int32_t t = te; t >= t0; --t) {
+      const int b = (te - t) & 1;
       // LDS and cache offsets are formed anew in each turn (a few instructions): kept in registers
       // through the loop, they push operands out to scratch memory
       if constexpr (D == 256) asm volatile("" : "+v"(tid));
       There<D> after = nxt;
-      if (t + 1 < t1) {
-        const bool bad2 = stage<D, BF16>(f, nxt, whole(t + 1, nxt), lds.tiles[b ^ 1][0], lds.tiles[b ^ 1][1], tid);
+      if (t > t0) {
+        const bool bad2 = stage<D, BF16>(f, nxt, whole(t - 1, nxt), lds.tiles[b ^ 1][0], lds.tiles[b ^ 1][1], tid);
         if (lane == 0) lds.nans[b ^ 1][wave] = bad2;
-        if (wave == kLookUp + (t & 3)) put_slots(t + 3);
-        // positions past the last tile have no slot; they read slot 0 and are not used
-        fetch<D>(a, lds.slots[(t + 2) & 3], lds.in_cache[(t + 2) & 3], kbase, vbase, tid, f, after);
-        if (wave == kLookUp + ((t + 1) & 3)) load_entries(t + 4);
+        if (wave == kLookUp + (t & 3)) put_slots(t - 3);
+        // tiles before the first have negative positions, which have no slot: they read slot 0 and are not used
+        fetch<D>(a, lds.slots[(t - 2) & 3], lds.in_cache[(t - 2) & 3], kbase, vbase, tid, f, after);
+        if (wave == kLookUp + ((t - 1) & 3)) load_entries(t - 4);
       }
       const int32_t j0 = t * BN;
       if (j0 < s.hi_max && j0 + BN > s.lo_min) {
