@@ -33,43 +33,58 @@ constexpr int kUnit = kWaves * kStep;  // positions of a workgroup's step
 // Workgroups that share a compute unit's registers: what a call is divided among.  More of them keep more
 // loads in flight, as long as their operands fit: 4 KB a step and wavefront with 64 dims, 16 KB with 256.
 constexpr int stream_groups(int head_dim, int rows) {
-  if (head_dim == 64) return rows == 16 ? 4 : (rows == 32 ? 2 : 1);
-  if (head_dim == 128) return rows <= 32 ? 2 : 1;
+  if (head_dim == 64) return rows <= 32 ? 3 : 2;
+  if (head_dim == 128) return rows == 16 ? 3 : (rows == 32 ? 2 : 1);
   return 1;
 }
 
 // Codes of 32 positions as a lane holds them.
 template <int D>
-struct Codes {
-  u32x4 k[2][D / 64];        // keys l % 16 and 16 + l % 16
-  uint32_t v[8][D / 64];     // keys 4 g + i and 16 + 4 g + i
+struct Keys {
+  u32x4 k[2][D / 64];  // keys l % 16 and 16 + l % 16
 };
 
 template <int D>
-__device__ __forceinline__ void load_codes(const AttnArgs& a, int32_t slot, const uint8_t* kbase,
-                                           const uint8_t* vbase, int lane, Codes<D>& c) {
-  // a position that is not in the cache reads slot 0 (there is one) and is masked afterwards
+struct Values {
+  uint32_t v[8][D / 64];  // keys 4 g + i and 16 + 4 g + i
+};
+
+// A position that is not in the cache reads slot 0 (there is one) and is masked afterwards.  Every line is
+// read by one workgroup once, so the loads do not ask to be kept in the caches -- except those of keys
+// of 64 and 128 dims, whose lines are read in two or more goes (64 x 8000 positions, 128 dims: values
+// kept 131 us, not kept 122 us, nothing kept 131 us; 256 dims: 128, 120 and 116 us).
+template <int D>
+__device__ __forceinline__ void load_keys(const AttnArgs& a, int32_t slot, const uint8_t* kbase, int lane, Keys<D>& c) {
   const int32_t s = slot < 0 ? 0 : slot;
-  const int g = lane >> 4, d16 = lane & 15;
+  const uint8_t* base = kbase + (lane >> 4) * 16;
+  const int from = (lane & 15) * 4;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const int32_t sk = __shfl(s, 16 * t + d16);
-    const uint8_t* p = row_at(kbase, sk, a) + g * 16;
+    const uint8_t* p = row_at(base, __builtin_amdgcn_ds_bpermute(from + 64 * t, s), a);
 #pragma unroll
-    for (int j = 0; j < D / 64; ++j) c.k[t][j] = *reinterpret_cast<const u32x4*>(p + 64 * j);
+    for (int j = 0; j < D / 64; ++j) {
+      const u32x4* q = reinterpret_cast<const u32x4*>(p + 64 * j);
+      c.k[t][j] = D == 256 ? __builtin_nontemporal_load(q) : *q;
+    }
   }
+}
+
+template <int D>
+__device__ __forceinline__ void load_values(const AttnArgs& a, int32_t slot, const uint8_t* vbase, int lane, Values<D>& c) {
+  const int32_t s = slot < 0 ? 0 : slot;
+  const uint8_t* base = vbase + (lane & 15) * (D / 16);
+  const int from = (lane >> 4) * 16;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const int32_t sv = __shfl(s, 16 * (e >> 2) + 4 * g + (e & 3));
-    const uint8_t* p = row_at(vbase, sv, a) + d16 * (D / 16);
+    const uint8_t* p = row_at(base, __builtin_amdgcn_ds_bpermute(from + (16 * (e >> 2) + (e & 3)) * 4, s), a);
     if constexpr (D == 256) {
-      const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+      const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
       c.v[e][0] = w.x; c.v[e][1] = w.y; c.v[e][2] = w.z; c.v[e][3] = w.w;
     } else if constexpr (D == 128) {
-      const u32x2 w = *reinterpret_cast<const u32x2*>(p);
+      const u32x2 w = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
       c.v[e][0] = w.x; c.v[e][1] = w.y;
     } else {
-      c.v[e][0] = *reinterpret_cast<const uint32_t*>(p);
+      c.v[e][0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
     }
   }
 }
@@ -97,14 +112,15 @@ struct State {
   u32x4 q[NQ][D / 32];
   f32x4 acc[NQ][D / 16];  // acc[.][t][i]: dim (4 g + i) * (D / 16) + t
   float m[NQ], l[NQ];     // l: this lane's keys only
-  Row row[NQ];
+  int32_t lo[NQ], hi[NQ];  // of the lane's rows, as in Row; their numbers are formed again where needed
+  int32_t pos[NQ];
+  float slope[NQ];
   int32_t lo_all, hi_all;  // positions every row of the tile sees: [lo_all, hi_all)
 };
 
-template <int D, bool BF16, int NQ>
-__device__ __forceinline__ void step(const AttnArgs& a, const Request& rq, Codes<D>& c, int32_t slot,
-                                     const uint8_t* vbase,
-                                     int32_t j0, float mul, float inv_cap, int lane, State<D, NQ>& s) {
+template <int D, bool BF16, int NQ, bool MODS>
+__device__ __forceinline__ void step(const Segment& sg, const Request& rq, const Keys<D>& kc, Values<D>& vc, int32_t slot,
+                                     int32_t j0, float c, float cap, int lane, State<D, NQ>& s) {
   const int g = lane >> 4;
   f32x4 x[2][NQ];
 #pragma unroll
@@ -117,11 +133,13 @@ __device__ __forceinline__ void step(const AttnArgs& a, const Request& rq, Codes
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const u32x2 lo = decode_key<BF16>(c.k[t][j][2 * h]);
-        const u32x2 hi = decode_key<BF16>(c.k[t][j][2 * h + 1]);
+        const u32x2 lo = decode_key<BF16>(kc.k[t][j][2 * h]);
+        const u32x2 hi = decode_key<BF16>(kc.k[t][j][2 * h + 1]);
         const u32x4 k = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
         for (int n = 0; n < NQ; ++n) x[t][n] = mfma16<BF16>(k, s.q[n][2 * j + h], x[t][n]);
+        // decode a few operands at a time: all of them at once take twice the registers of their codes
+        if (t == 1) __builtin_amdgcn_sched_barrier(0);
       }
 
   __builtin_amdgcn_sched_barrier(0);  // the phases' instructions stay apart, to keep their registers few
@@ -129,17 +147,19 @@ __device__ __forceinline__ void step(const AttnArgs& a, const Request& rq, Codes
   const uint64_t in_cache = __ballot(slot >= 0);
   const bool whole = in_cache == ~0ull && j0 >= s.lo_all && j0 + kStep <= s.hi_all;
   // scores are x cm + base, in units of log2
-  float cm = mul * kLog2e, base = 0.0f;
-  if (a.cap > 0.0f) {
-    const float to_r = cm * inv_cap * 2.0f;
+  float cm = c, base = 0.0f;
+  if constexpr (MODS) {
+    if (cap > 0.0f) {
+      const float to_r = cm / cap * 2.0f;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int n = 0; n < NQ; ++n)
+        for (int n = 0; n < NQ; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[t][n][i] = cap_term(x[t][n][i], to_r);
-    base = a.cap * kLog2e;
-    cm = -2.0f * base;
+          for (int i = 0; i < 4; ++i) x[t][n][i] = cap_term(x[t][n][i], to_r);
+      base = cap * kLog2e;
+      cm = -2.0f * base;
+    }
   }
 #pragma unroll
   for (int t = 0; t < 2; ++t)
@@ -147,25 +167,29 @@ __device__ __forceinline__ void step(const AttnArgs& a, const Request& rq, Codes
     for (int n = 0; n < NQ; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[t][n][i] = __builtin_fmaf(x[t][n][i], cm, base);
-  if (a.slopes) {
-    const int32_t* positions = a.tree ? a.positions : nullptr;
+  if constexpr (MODS) {
+    const AttnArgs& a = args();
+    if (a.slopes) {
+      const int32_t* positions = a.tree ? a.positions : nullptr;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int32_t kp = key_position(positions, rq, j0 + 16 * t + 4 * g + i);
+        for (int i = 0; i < 4; ++i) {
+          const int32_t kp = key_position(positions, rq, j0 + 16 * t + 4 * g + i);
 #pragma unroll
-        for (int n = 0; n < NQ; ++n)
-          x[t][n][i] = __builtin_fmaf(s.row[n].slope, (float)(kp - s.row[n].pos), x[t][n][i]);
-      }
+          for (int n = 0; n < NQ; ++n)
+            x[t][n][i] = __builtin_fmaf(s.slope[n], (float)(kp - s.pos[n]), x[t][n][i]);
+        }
+    }
   }
   // bit 16 t + i of seen[n] >> 4 g: whether row n sees position 16 t + 4 g + i of the step
   uint32_t seen[NQ];
-  const bool tree = a.tree != nullptr;
   if (rarely(!whole)) {
+    const AttnArgs& a = args();
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      seen[n] = ((uint32_t)sees64(s.row[n].lo, s.row[n].hi, tree ? s.row[n].token : -1, rq.ctx, j0) & (uint32_t)in_cache) >> (4 * g);
+      const int32_t token = a.tree ? token_of(a, rq, (uint32_t)((sg.tile * NQ + n) * 16 + (lane & 15))) : -1;
+      seen[n] = ((uint32_t)sees64(s.lo[n], s.hi[n], token, rq.ctx, j0) & (uint32_t)in_cache) >> (4 * g);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -204,31 +228,29 @@ __device__ __forceinline__ void step(const AttnArgs& a, const Request& rq, Codes
   __builtin_amdgcn_sched_barrier(0);
   bool nans = false;
   if (rarely(!whole)) {
+    const uint32_t mine = (uint32_t)in_cache >> (4 * g);  // bit 16 t + i: position 16 t + 4 g + i
     uint32_t bad = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const bool there = (in_cache >> (16 * (e >> 2) + 4 * g + (e & 3))) & 1;
+      const uint32_t there = (uint32_t)((int32_t)(mine << (31 - (16 * (e >> 2) + (e & 3)))) >> 31);
 #pragma unroll
       for (int d = 0; d < D / 64; ++d) {
-        c.v[e][d] = there ? c.v[e][d] : 0u;
-        bad |= nan_codes(c.v[e][d]);
+        vc.v[e][d] &= there;
+        const uint32_t b = nan_codes(vc.v[e][d]);
+        bad |= b;
+        vc.v[e][d] &= ~((b >> 7) * 0xFFu);
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
     nans = __any(bad != 0);
-    if (rarely(nans)) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-#pragma unroll
-        for (int d = 0; d < D / 64; ++d) c.v[e][d] = without_nans(c.v[e][d]);
-    }
   }
 #pragma unroll
   for (int d = 0; d < D / 64; ++d) {
     uint32_t a0[4], a1[4], t0[4], t1[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      a0[i] = c.v[i][d];
-      a1[i] = c.v[4 + i][d];
+      a0[i] = vc.v[i][d];
+      a1[i] = vc.v[4 + i][d];
     }
     transpose4(a0, t0);
     transpose4(a1, t1);
@@ -239,8 +261,11 @@ __device__ __forceinline__ void step(const AttnArgs& a, const Request& rq, Codes
 #pragma unroll
       for (int n = 0; n < NQ; ++n) s.acc[n][4 * d + b] = mfma16<false>(w, p[n], s.acc[n][4 * d + b]);
     }
+    __builtin_amdgcn_sched_barrier(0);
   }
   if (rarely(nans)) {
+    const AttnArgs& a = args();
+    const uint8_t* vbase = a.vc + (int64_t)sg.kv_head * D;
 #pragma unroll 1
     for (int o = 0; o < kStep; ++o) {
       const int32_t at = __shfl(slot, o);
@@ -249,7 +274,8 @@ __device__ __forceinline__ void step(const AttnArgs& a, const Request& rq, Codes
       const uint8_t* p8 = row_at(vbase, at, a) + g * (D / 4);
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
-        const bool see = ((uint32_t)sees64(s.row[n].lo, s.row[n].hi, tree ? s.row[n].token : -1, rq.ctx, j0) >> o) & 1;
+        const int32_t token = a.tree ? token_of(a, rq, (uint32_t)((sg.tile * NQ + n) * 16 + (lane & 15))) : -1;
+        const bool see = (sees64(s.lo[n], s.hi[n], token, rq.ctx, j0) >> o) & 1;
 #pragma unroll
         for (int w = 0; w < D / 16; ++w) {
           const uint32_t bad = see ? nan_codes(*reinterpret_cast<const uint32_t*>(p8 + 4 * w)) : 0u;
@@ -265,8 +291,8 @@ __device__ __forceinline__ void step(const AttnArgs& a, const Request& rq, Codes
   }
 }
 
-template <int D, bool BF16, int NQ>
-__device__ __forceinline__ void segment(const Segment& sg, bool split, float* lds) {
+template <int D, bool BF16, int NQ, bool MODS>
+__device__ __forceinline__ void segment(const Segment& sg, bool split, int32_t worker, float* lds) {
   const AttnArgs& a = args();
   constexpr int kRows = 16 * NQ;
   constexpr int kPitch = D + 4;  // floats; 16 bytes a row apart, so a store's 8 lanes differ in banks
@@ -274,14 +300,16 @@ __device__ __forceinline__ void segment(const Segment& sg, bool split, float* ld
   const int g = lane >> 4, d16 = lane & 15;
   const Request rq = request_of(a, sg.r);
   State<D, NQ> s;
-  const float mul = a.scale * *a.ks;
-  const float inv_cap = a.cap > 0.0f ? 1.0f / a.cap : 0.0f;
+  const float c = a.scale * *a.ks * kLog2e, cap = MODS ? a.cap : 0.0f;
 
   int32_t lo_min = 0x7FFFFFFF, hi_max = 0, lo_max = 0, hi_min = 0x7FFFFFFF;
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     const Row w = row_of(a, sg.r, rq, sg.kv_head, (uint32_t)(sg.tile * kRows + 16 * n + d16));
-    s.row[n] = w;
+    s.lo[n] = w.lo;
+    s.hi[n] = w.hi;
+    s.pos[n] = w.pos;
+    s.slope[n] = w.slope;
     s.m[n] = kNoScore;
     s.l[n] = 0.0f;
 #pragma unroll
@@ -332,18 +360,30 @@ __device__ __forceinline__ void segment(const Segment& sg, bool split, float* ld
     int32_t u = u1 - 1;
     int32_t s0 = slots(entries(u), u), s1;
     int32_t e1 = entries(u - 1);
-    Codes<D> c0, c1;
-    load_codes<D>(a, s0, kbase, vbase, lane, c0);
+    __builtin_amdgcn_sched_barrier(0);
+    Keys<D> k0, k1;
+    Values<D> v;
+    load_keys<D>(a, s0, kbase, lane, k0);
     for (;; u -= 2) {
+      // lane offsets are formed anew in each turn: kept through the loop, they push operands out to
+      // scratch memory, and reading those back waits for the codes in flight
+      int ln = lane;
+      asm volatile("" : "+v"(ln));
+      // (table entries are requested ahead of the codes: loads land in order, and looking at an entry
+      // that was requested after them would wait for the codes)
       s1 = slots(e1, u - 1);
-      if (u > u0) load_codes<D>(a, s1, kbase, vbase, lane, c1);
       const int32_t e2 = entries(u - 2);
-      step<D, BF16, NQ>(a, rq, c0, s0, vbase, u * kUnit + wave * kStep, mul, inv_cap, lane, s);
+      __builtin_amdgcn_sched_barrier(0);
+      load_values<D>(a, s0, vbase, ln, v);
+      if (u > u0) load_keys<D>(a, s1, kbase, ln, k1);
+      step<D, BF16, NQ, MODS>(sg, rq, k0, v, s0, u * kUnit + wave * kStep, c, cap, ln, s);
       if (u - 1 < u0) break;
       s0 = slots(e2, u - 2);
-      if (u - 1 > u0) load_codes<D>(a, s0, kbase, vbase, lane, c0);
       e1 = entries(u - 3);
-      step<D, BF16, NQ>(a, rq, c1, s1, vbase, (u - 1) * kUnit + wave * kStep, mul, inv_cap, lane, s);
+      __builtin_amdgcn_sched_barrier(0);
+      load_values<D>(a, s1, vbase, ln, v);
+      if (u - 1 > u0) load_keys<D>(a, s0, kbase, ln, k0);
+      step<D, BF16, NQ, MODS>(sg, rq, k1, v, s1, (u - 1) * kUnit + wave * kStep, c, cap, ln, s);
       if (u - 2 < u0) break;
     }
   }
@@ -397,7 +437,7 @@ __device__ __forceinline__ void segment(const Segment& sg, bool split, float* ld
     const uint32_t rr = (uint32_t)(sg.tile * kRows + 16 * n + row);
     if (rr < (uint32_t)rq.count * ea.group.d) {
       if (split && !(sg.first && sg.last)) {
-        const int64_t at = part_slot(blockIdx.x, sg.first) * kRows + 16 * n + row;
+        const int64_t at = part_slot((uint32_t)worker, sg.first) * kRows + 16 * n + row;
         float* op = ea.part + at * D + part * (D / 16);
 #pragma unroll
         for (int t = 0; t < D / 16; t += 4) *reinterpret_cast<f32x4*>(op + t) = f32x4{o[t], o[t + 1], o[t + 2], o[t + 3]};
@@ -416,7 +456,7 @@ __device__ __forceinline__ void segment(const Segment& sg, bool split, float* ld
   __syncthreads();  // the next segment writes ml and the tiles again
 }
 
-template <int D, bool BF16, int NQ>
+template <int D, bool BF16, int NQ, bool MODS>
 __global__ void __launch_bounds__(kThreads, stream_groups(D, 16 * NQ)) attention_stream_kernel(AttnArgs) {
   constexpr int kRows = 16 * NQ;
   __shared__ __align__(16) float lds[kWaves * 16 * (D + 4) + kWaves * kRows * 2];
@@ -432,31 +472,31 @@ __global__ void __launch_bounds__(kThreads, stream_groups(D, 16 * NQ)) attention
     s.u0 = 0;
     s.u1 = (int32_t)(((uint32_t)q.len + kUnit - 1) / kUnit);
     const int32_t tiles = (int32_t)(((uint32_t)q.count * a.group.d + kRows - 1) / kRows);
-    for (s.tile = blockIdx.z; s.tile < tiles; s.tile += gridDim.z) segment<D, BF16, NQ>(s, false, lds);
+    for (s.tile = blockIdx.z; s.tile < tiles; s.tile += gridDim.z) segment<D, BF16, NQ, MODS>(s, false, 0, lds);
     return;
   }
   share.begin(kRows, kUnit);
-  int32_t* header = args().headers + 4 * blockIdx.x;
-  if (threadIdx.x == 0) *reinterpret_cast<Header*>(header) = Header{0, 0, 0, -1};
+  Header* header = reinterpret_cast<Header*>(args().headers) + blockIdx.x;
+  if (threadIdx.x == 0) header->last_worker = -1;
   while (share.next(kRows, kUnit, s)) {
-    if (s.first && !s.last && threadIdx.x == 0) *reinterpret_cast<Header*>(header) = Header{s.r, s.tile, s.kv_head, s.last_worker};
-    segment<D, BF16, NQ>(s, true, lds);
+    if (s.first && !s.last && threadIdx.x == 0) *header = Header{s.r, s.tile, s.kv_head, s.last_worker, share.worker, {0, 0, 0}};
+    segment<D, BF16, NQ, MODS>(s, true, uniform(share.worker), lds);
   }
 }
 
-// Joins the pieces of the items that were shared out: block (w, y) takes four rows of the item that
-// begins in worker w and ends in worker last_worker, a wavefront each.  The pieces are summed in the
+// Joins the pieces of the items that were shared out: block (b, y) takes rows of the item that
+// begins in workgroup b's share and ends in worker last_worker, a wavefront each.  The pieces are summed in the
 // workers' order, whatever order they were computed in.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads) attention_join_kernel(AttnArgs a, int32_t rows) {
-  const Header h = *reinterpret_cast<const Header*>(a.headers + 4 * blockIdx.x);
+  const Header h = reinterpret_cast<const Header*>(a.headers)[blockIdx.x];
   if (h.last_worker < 0) return;
   const Request rq = request_of(a, h.r);
   const int lane = threadIdx.x & 63;
   const int32_t local = blockIdx.y * kWaves + (threadIdx.x >> 6);
   const uint32_t rr = (uint32_t)(h.tile * rows + local);
   if (rr >= (uint32_t)rq.count * a.group.d) return;
-  const uint32_t w0 = blockIdx.x;
+  const uint32_t w0 = (uint32_t)h.worker;
   const int32_t n = h.last_worker - (int32_t)w0 + 1;
   constexpr int E = D / 64;
   float m = kNoScore;
@@ -496,10 +536,18 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(AttnArgs a, in
   }
 }
 
-template <int D, bool BF16, int NQ>
+template <int D, bool BF16, int NQ, bool MODS>
 void launch_stream(const AttnArgs& a, hipStream_t stream) {
   const dim3 grid = a.workers ? dim3((uint32_t)a.workers) : dim3((uint32_t)a.kv_heads, (uint32_t)a.requests, (uint32_t)a.row_tiles);
-  hipLaunchKernelGGL((attention_stream_kernel<D, BF16, NQ>), grid, dim3(kThreads), 0, stream, a);
+  hipLaunchKernelGGL((attention_stream_kernel<D, BF16, NQ, MODS>), grid, dim3(kThreads), 0, stream, a);
+}
+
+template <int D, bool BF16, int NQ>
+void launch_stream(const AttnArgs& a, hipStream_t stream) {
+  if (a.cap > 0.0f || a.slopes)
+    launch_stream<D, BF16, NQ, true>(a, stream);
+  else
+    launch_stream<D, BF16, NQ, false>(a, stream);
 }
 
 template <int D, bool BF16>
@@ -549,7 +597,7 @@ AttnPlan plan_attention(int64_t heads, int64_t kv_heads, int64_t head_dim, int64
     p.workers = stream_groups((int)head_dim, p.rows) * kComputeUnits;
   }
   if (p.workers)
-    p.workspace = (int64_t)p.workers * (2 * (int64_t)p.rows * (head_dim + 2) + 4) * (int64_t)sizeof(float);
+    p.workspace = (int64_t)p.workers * (2 * (int64_t)p.rows * (head_dim + 2) + 8) * (int64_t)sizeof(float);
   return p;
 }
 

@@ -269,10 +269,12 @@ struct Segment {
   int32_t last_worker;  // worker that holds the item's last unit
 };
 
-// Headers that the workers leave for the joining kernel.
+// What every workgroup leaves for the joining kernel.
 struct Header {
   int32_t r, tile, kv_head;
   int32_t last_worker;  // of the item that begins in this worker and ends in a later one, else -1
+  int32_t worker;
+  int32_t unused[3];
 };
 
 // Work of request r in units, all its items: every item counts the units of the whole request.  (An
@@ -297,6 +299,14 @@ __device__ __forceinline__ uint64_t quotient(uint64_t n, uint64_t d) {
   return ((n | d) >> 32) == 0 ? (uint32_t)n / (uint32_t)d : n / d;
 }
 
+// Workgroup b runs on XCD b % 8, so worker numbers run through one XCD after another: workers next to
+// each other, which read the same rows for neighbouring KV heads, share an L2 (with 64 dims two heads
+// share every cache line).
+__device__ __forceinline__ uint32_t worker_of(uint32_t b, uint32_t P) {
+  const uint32_t per = (P + 7) / 8, k = b / 8;
+  return k < per ? (b % 8) * per + k : 0xFFFFFFFFu;
+}
+
 // The workers' shares: worker w takes units [W w / P, W (w + 1) / P) of the W units of all items, one
 // after another.  Every workgroup finds its own start by summing the requests' weights (one pass over
 // the lengths, or two where there are more requests than threads), with no launch before it and
@@ -312,6 +322,7 @@ struct Share {
   uint32_t units;      // of an item of request r
   uint32_t P;
   int32_t r;
+  int32_t worker;  // this workgroup's number
   int32_t more;
   Segment segment;
 
@@ -352,11 +363,12 @@ struct Share {
     // a worker takes two units at least: smaller shares cost more to join than to compute
     const uint64_t most = (sum + 1) / 2, limit = (uint64_t)a.workers;
     const uint32_t p = (uint32_t)(most < limit ? (most > 0 ? most : 1) : limit);
-    const uint32_t w = blockIdx.x;
+    const uint32_t w = worker_of(blockIdx.x, p);
     const uint64_t x0 = w < p ? quotient(sum * w, p) : 0, x1 = w < p ? quotient(sum * (w + 1), p) : 0;
     if (tid == 0) {
       W = sum;
       P = p;
+      worker = (int32_t)w;
       x = x0;
       end = x1;
       r = 0;

@@ -515,7 +515,7 @@ __device__ __forceinline__ void segment(const Segment& sg, Shared<D>& lds) {
     const Segment& now = lds.share.segment;
     const bool first = uniform(now.first), last = uniform(now.last);
     if (SPLIT && !(first && last)) {
-      const int64_t at = part_slot(blockIdx.x, first) * kRows + 32 * wave + r;
+      const int64_t at = part_slot((uint32_t)uniform(lds.share.worker), first) * kRows + 32 * wave + r;
       float* op = ea.part + at * D + 4 * h;
 #pragma unroll
       for (int d = 0; d < D / 32; ++d)
@@ -561,10 +561,10 @@ __global__ void __launch_bounds__(kThreads) attention_tiled_kernel(AttnArgs) {
     }
   } else {
     lds.share.begin(kRows, kKeys<D>);
-    int32_t* header = args().headers + 4 * blockIdx.x;
-    if (threadIdx.x == 0) *reinterpret_cast<Header*>(header) = Header{0, 0, 0, -1};
+    Header* header = reinterpret_cast<Header*>(args().headers) + blockIdx.x;
+    if (threadIdx.x == 0) header->last_worker = -1;
     while (lds.share.next(kRows, kKeys<D>, s)) {
-      if (s.first && !s.last && threadIdx.x == 0) *reinterpret_cast<Header*>(header) = Header{s.r, s.tile, s.kv_head, s.last_worker};
+      if (s.first && !s.last && threadIdx.x == 0) *header = Header{s.r, s.tile, s.kv_head, s.last_worker, lds.share.worker, {0, 0, 0}};
       segment<D, BF16, MODS, true>(s, lds);
     }
   }
