@@ -52,6 +52,8 @@ def declare(lib: ctypes.CDLL) -> None:
 
 def _vector(t, n, dtype, device, name):
     """``t`` must be a contiguous ``dtype`` vector of ``n`` elements on ``device``; returns its address."""
+    if t.dtype is dtype and t.shape == (n,) and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
@@ -75,11 +77,15 @@ def _table(t, rows, device, name):
 def _call(device, fn, *args):
     """Run one library call on ``device`` and its current stream, whichever device is current."""
     torch = _base._torch()
-    if torch.cuda.current_device() == device.index:
-        _base._check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+    # the stream's handle without a Stream object: 0.2 us of a call's 10 instead of 4
+    raw_stream, index = torch._C._cuda_getCurrentRawStream, device.index
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, raw_stream(index))
     else:
         with torch.cuda.device(device):
-            _base._check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+            status = fn(*args, raw_stream(index))
+    if status:
+        _base._check(status)
 
 
 def _cuda(t, name):

@@ -52,6 +52,7 @@ enum class AttnKernel : int32_t {
 struct AttnPlan {
   AttnKernel kernel;
   int32_t rows;     // query rows (token, head of the group) of a row tile
+  int32_t join_rows;  // of them, as many as the longest request has
   int32_t workers;  // 0: one workgroup per (row tile, KV head, request); else the number of
                     // workgroups that share the whole key range, and a joining launch
   int64_t workspace;

@@ -484,55 +484,96 @@ __global__ void __launch_bounds__(kThreads, stream_groups(D, 16 * NQ)) attention
   }
 }
 
-// Joins the pieces of the items that were shared out: block (b, y) takes rows of the item that
-// begins in workgroup b's share and ends in worker last_worker, a wavefront each.  The pieces are summed in the
-// workers' order, whatever order they were computed in.
+// Pieces [k0, k1) of one row of an item that several workers computed, under the reference m: their sums
+// of exponentials (l, the same in every lane) and of outputs (this lane's D / 64 dims).  Pieces are summed
+// in the workers' order, whatever order they were computed in.
+template <int D>
+__device__ __forceinline__ void join_pieces(const AttnArgs& a, const Header& h, int32_t rows, int32_t local, int32_t k0,
+                                            int32_t k1, float m, int lane, float& l, float (&o)[D / 64]) {
+  constexpr int E = D / 64, kAtOnce = 16;
+  const uint32_t w0 = (uint32_t)h.worker;
+  l = 0.0f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.0f;
+  for (int32_t b = k0; b < k1; b += kAtOnce) {
+    // kAtOnce pieces are requested together; past the last, the last again, with weight 0
+    float v[kAtOnce][E];
+    const int32_t mine = min(b + (lane & (kAtOnce - 1)), k1 - 1);
+    const f32x2 ml = *reinterpret_cast<const f32x2*>(a.part_ml + 2 * (part_slot(w0 + mine, mine == 0) * rows + local));
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int32_t at = min(b + k, k1 - 1);
+      const float* p = a.part + (part_slot(w0 + at, at == 0) * rows + local) * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[k][e] = p[e];
+    }
+    const float f = exp2_of(ml.x - m);
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const bool there = b + k < k1;
+      const float fk = __shfl(f, k), lk = __shfl(ml.y, k);
+      l = there ? __builtin_fmaf(lk, fk, l) : l;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = there ? __builtin_fmaf(v[k][e], fk, o[e]) : o[e];
+    }
+  }
+}
+
+// Joins the pieces of the items that were shared out: blocks (b, y) take rows of the item that begins in
+// workgroup b's share and ends in that of worker last_worker.  With few pieces a wavefront takes a whole
+// row and a block four; with more (one long request over all workers) a block takes one row and its
+// wavefronts a quarter of the pieces each.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads) attention_join_kernel(AttnArgs a, int32_t rows) {
+  constexpr int E = D / 64;
+  __shared__ float sums[kWaves][D + 1];
   const Header h = reinterpret_cast<const Header*>(a.headers)[blockIdx.x];
   if (h.last_worker < 0) return;
   const Request rq = request_of(a, h.r);
-  const int lane = threadIdx.x & 63;
-  const int32_t local = blockIdx.y * kWaves + (threadIdx.x >> 6);
-  const uint32_t rr = (uint32_t)(h.tile * rows + local);
-  if (rr >= (uint32_t)rq.count * a.group.d) return;
-  const uint32_t w0 = (uint32_t)h.worker;
-  const int32_t n = h.last_worker - (int32_t)w0 + 1;
-  constexpr int E = D / 64;
-  float m = kNoScore;
-  for (int32_t k = lane; k < n; k += 64) m = __builtin_fmaxf(m, a.part_ml[2 * (part_slot(w0 + k, k == 0) * rows + local)]);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int32_t n = h.last_worker - h.worker + 1;
+  const bool alone = n <= 16;  // a wavefront joins a row by itself
+  const int32_t per = alone ? kWaves : 1;
+  for (int32_t first = (int32_t)blockIdx.y * per; first < rows; first += (int32_t)gridDim.y * per) {
+    const int32_t local = alone ? first + wave : first;
+    const uint32_t row = (uint32_t)(h.tile * rows + local);
+    const int32_t token = token_of(a, rq, row);
+    if (!alone && token < 0) return;  // the same in all wavefronts; so are later rows
+    if (token < 0) continue;
+    float m = kNoScore;
+    for (int32_t k = lane; k < n; k += 64)
+      m = __builtin_fmaxf(m, a.part_ml[2 * (part_slot((uint32_t)(h.worker + k), k == 0) * rows + local)]);
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) m = __builtin_fmaxf(m, __shfl_xor(m, d));
-  float o[E], l = 0.0f;
+    for (int d = 1; d < 64; d <<= 1) m = __builtin_fmaxf(m, __shfl_xor(m, d));
+    float o[E], l;
+    const int32_t share = (n + kWaves - 1) / kWaves;
+    join_pieces<D>(a, h, rows, local, alone ? 0 : min(wave * share, n), alone ? n : min((wave + 1) * share, n), m, lane, l, o);
+    if (!alone) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.0f;
-  for (int32_t b = 0; b < n; b += 64) {
-    float f = 0.0f, lk = 0.0f;
-    if (b + lane < n) {
-      const f32x2 v = *reinterpret_cast<const f32x2*>(a.part_ml + 2 * (part_slot(w0 + b + lane, b + lane == 0) * rows + local));
-      f = exp2_of(v.x - m);
-      lk = v.y * f;
+      for (int e = 0; e < E; ++e) sums[wave][lane * E + e] = o[e];
+      if (lane == 0) sums[wave][D] = l;
+      __syncthreads();
+      l = 0.0f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        l += sums[w][D];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += sums[w][lane * E + e];
+      }
+      __syncthreads();
+      if (wave != 0) continue;
     }
-    const int32_t c = min(64, n - b);
-#pragma unroll 8
-    for (int32_t k = 0; k < c; ++k) {
-      const float* p = a.part + (part_slot(w0 + b + k, b + k == 0) * rows + local) * D + lane * E;
-      const float fk = __shfl(f, k);
-      l += __shfl(lk, k);
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = __builtin_fmaf(p[e], fk, o[e]);
+    const float inv = l == 0.0f ? 0.0f : *a.vs / l;
+    uint16_t* op = a.out + (int64_t)token * a.out_ts + (int64_t)head_of(a, rq, h.kv_head, row) * a.out_hs + lane * E;
+    if constexpr (E == 1) {
+      *op = (uint16_t)pack_out<BF16>(o[0] * inv, 0.0f);
+    } else if constexpr (E == 2) {
+      *reinterpret_cast<uint32_t*>(op) = pack_out<BF16>(o[0] * inv, o[1] * inv);
+    } else {
+      *reinterpret_cast<u32x2*>(op) = u32x2{pack_out<BF16>(o[0] * inv, o[1] * inv), pack_out<BF16>(o[2] * inv, o[3] * inv)};
     }
-  }
-  const float inv = l == 0.0f ? 0.0f : *a.vs / l;
-  const int32_t i = (int32_t)div_of(rr, a.group);
-  const int32_t head = h.kv_head * (int32_t)a.group.d + (int32_t)(rr - (uint32_t)i * a.group.d);
-  uint16_t* op = a.out + (int64_t)(rq.start + i) * a.out_ts + (int64_t)head * a.out_hs + lane * E;
-  if constexpr (E == 1) {
-    *op = (uint16_t)pack_out<BF16>(o[0] * inv, 0.0f);
-  } else if constexpr (E == 2) {
-    *reinterpret_cast<uint32_t*>(op) = pack_out<BF16>(o[0] * inv, o[1] * inv);
-  } else {
-    *reinterpret_cast<u32x2*>(op) = u32x2{pack_out<BF16>(o[0] * inv, o[1] * inv), pack_out<BF16>(o[2] * inv, o[3] * inv)};
   }
 }
 
@@ -566,8 +607,10 @@ hipError_t launch_all(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) 
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.workers == 0) return e;
-  hipLaunchKernelGGL((attention_join_kernel<D, BF16>), dim3((uint32_t)a.workers, (uint32_t)(p.rows / kWaves)),
-                     dim3(kThreads), 0, stream, a, p.rows);
+  // enough blocks for the rows that a tile has as far as the caller told, one row or four a block; the
+  // kernel's stride covers the others
+  const uint32_t y = (uint32_t)(p.join_rows <= 16 ? p.join_rows : (p.join_rows + kWaves - 1) / kWaves);
+  hipLaunchKernelGGL((attention_join_kernel<D, BF16>), dim3((uint32_t)a.workers, y), dim3(kThreads), 0, stream, a, p.rows);
   return hipGetLastError();
 }
 
@@ -590,6 +633,7 @@ AttnPlan plan_attention(int64_t heads, int64_t kv_heads, int64_t head_dim, int64
     p.kernel = AttnKernel::Tiled;
     p.rows = 256;
   }
+  p.join_rows = (int32_t)(rows < p.rows ? rows : p.rows);
   const int64_t items = requests * kv_heads * ((rows + p.rows - 1) / p.rows);
   if (p.kernel == AttnKernel::Tiled) {
     if (max_seq_len > 256 && items < kComputeUnits) p.workers = kComputeUnits;
