@@ -43,9 +43,8 @@ struct TablesArgs {
 
 // How an attention call is divided among workgroups.
 enum class AttnKernel : int32_t {
-  Stream16,  // a wavefront streams its own keys past 16, 32 or 64 query rows
+  Stream16,  // a wavefront streams its own keys past 16 or 32 query rows
   Stream32,
-  Stream64,
   Tiled,  // key tiles staged in LDS for 256 query rows
 };
 

@@ -1,8 +1,8 @@
 // Attention of few query rows over the paged FP8 cache: decode steps, drafted trees, short chunks.
 // Also the kernel that joins partial results, and the rule that divides a call's work.
 //
-// What bounds it: every key and value code is read once per (request, KV head) and used by 16, 32 or
-// 64 rows, so the call is bound by HBM reads.  The kernel therefore keeps as many loads in flight as
+// What bounds it: every key and value code is read once per (request, KV head) and used by 16 or
+// 32 rows, so the call is bound by HBM reads.  The kernel therefore keeps as many loads in flight as
 // its registers hold and touches LDS only to join its wavefronts at the end of an item.  A wavefront
 // takes 32 positions at a time, from the cache straight into MFMA operand registers:
 //
@@ -33,8 +33,8 @@ constexpr int kUnit = kWaves * kStep;  // positions of a workgroup's step
 // Workgroups that share a compute unit's registers: what a call is divided among.  More of them keep more
 // loads in flight, as long as their operands fit: 4 KB a step and wavefront with 64 dims, 16 KB with 256.
 constexpr int stream_groups(int head_dim, int rows) {
-  if (head_dim == 64) return rows <= 32 ? 3 : 2;
-  if (head_dim == 128) return rows == 16 ? 3 : (rows == 32 ? 2 : 1);
+  if (head_dim == 64) return 3;
+  if (head_dim == 128) return rows == 16 ? 3 : 2;
   return 1;
 }
 
@@ -49,11 +49,20 @@ struct Values {
   uint32_t v[8][D / 64];  // keys 4 g + i and 16 + 4 g + i
 };
 
-// A position that is not in the cache reads slot 0 (there is one) and is masked afterwards.  Every line is
-// read by one workgroup once, so the loads do not ask to be kept in the caches -- except those of keys
-// of 64 and 128 dims, whose lines are read in two or more goes (64 x 8000 positions, 128 dims: values
-// kept 131 us, not kept 122 us, nothing kept 131 us; 256 dims: 128, 120 and 116 us).
-template <int D>
+template <bool ONCE, typename T>
+__device__ __forceinline__ T read(const T* p) {
+  if constexpr (ONCE) return __builtin_nontemporal_load(p);
+  return *p;
+}
+
+// A position that is not in the cache reads slot 0 (there is one) and is masked afterwards.  ONCE: the
+// request's rows fit one tile, every line is read by one workgroup once, and the loads do not ask to be
+// kept in the caches -- except those of keys of 64 and 128 dims, whose lines are read in two or more
+// goes (64 x 8000 positions, 128 dims: values kept 131 us, not kept 122 us, nothing kept 131 us; 256
+// dims: 128, 120 and 116 us).  Several row tiles of a request read the same lines at about the same
+// time, and asking for them to be kept pays (16 x 6001 positions, 3 tiles of 128 dims: 71 us, not kept
+// 78 us).
+template <int D, bool ONCE>
 __device__ __forceinline__ void load_keys(const AttnArgs& a, int32_t slot, const uint8_t* kbase, int lane, Keys<D>& c) {
   const int32_t s = slot < 0 ? 0 : slot;
   const uint8_t* base = kbase + (lane >> 4) * 16;
@@ -64,12 +73,12 @@ __device__ __forceinline__ void load_keys(const AttnArgs& a, int32_t slot, const
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
       const u32x4* q = reinterpret_cast<const u32x4*>(p + 64 * j);
-      c.k[t][j] = D == 256 ? __builtin_nontemporal_load(q) : *q;
+      c.k[t][j] = read<ONCE && D == 256>(q);
     }
   }
 }
 
-template <int D>
+template <int D, bool ONCE>
 __device__ __forceinline__ void load_values(const AttnArgs& a, int32_t slot, const uint8_t* vbase, int lane, Values<D>& c) {
   const int32_t s = slot < 0 ? 0 : slot;
   const uint8_t* base = vbase + (lane & 15) * (D / 16);
@@ -78,13 +87,13 @@ __device__ __forceinline__ void load_values(const AttnArgs& a, int32_t slot, con
   for (int e = 0; e < 8; ++e) {
     const uint8_t* p = row_at(base, __builtin_amdgcn_ds_bpermute(from + (16 * (e >> 2) + (e & 3)) * 4, s), a);
     if constexpr (D == 256) {
-      const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+      const u32x4 w = read<ONCE>(reinterpret_cast<const u32x4*>(p));
       c.v[e][0] = w.x; c.v[e][1] = w.y; c.v[e][2] = w.z; c.v[e][3] = w.w;
     } else if constexpr (D == 128) {
-      const u32x2 w = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
+      const u32x2 w = read<ONCE>(reinterpret_cast<const u32x2*>(p));
       c.v[e][0] = w.x; c.v[e][1] = w.y;
     } else {
-      c.v[e][0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
+      c.v[e][0] = read<ONCE>(reinterpret_cast<const uint32_t*>(p));
     }
   }
 }
@@ -363,7 +372,7 @@ __device__ __forceinline__ void segment(const Segment& sg, bool split, int32_t w
     __builtin_amdgcn_sched_barrier(0);
     Keys<D> k0, k1;
     Values<D> v;
-    load_keys<D>(a, s0, kbase, lane, k0);
+    load_keys<D, NQ == 1>(a, s0, kbase, lane, k0);
     for (;; u -= 2) {
       // lane offsets are formed anew in each turn: kept through the loop, they push operands out to
       // scratch memory, and reading those back waits for the codes in flight
@@ -374,15 +383,15 @@ __device__ __forceinline__ void segment(const Segment& sg, bool split, int32_t w
       s1 = slots(e1, u - 1);
       const int32_t e2 = entries(u - 2);
       __builtin_amdgcn_sched_barrier(0);
-      load_values<D>(a, s0, vbase, ln, v);
-      if (u > u0) load_keys<D>(a, s1, kbase, ln, k1);
+      load_values<D, NQ == 1>(a, s0, vbase, ln, v);
+      if (u > u0) load_keys<D, NQ == 1>(a, s1, kbase, ln, k1);
       step<D, BF16, NQ, MODS>(sg, rq, k0, v, s0, u * kUnit + wave * kStep, c, cap, ln, s);
       if (u - 1 < u0) break;
       s0 = slots(e2, u - 2);
       e1 = entries(u - 3);
       __builtin_amdgcn_sched_barrier(0);
-      load_values<D>(a, s1, vbase, ln, v);
-      if (u - 1 > u0) load_keys<D>(a, s0, kbase, ln, k0);
+      load_values<D, NQ == 1>(a, s1, vbase, ln, v);
+      if (u - 1 > u0) load_keys<D, NQ == 1>(a, s0, kbase, ln, k0);
       step<D, BF16, NQ, MODS>(sg, rq, k1, v, s1, (u - 1) * kUnit + wave * kStep, c, cap, ln, s);
       if (u - 2 < u0) break;
     }
@@ -596,9 +605,6 @@ hipError_t launch_all(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) 
   switch (p.kernel) {
     case AttnKernel::Stream16: launch_stream<D, BF16, 1>(a, stream); break;
     case AttnKernel::Stream32: launch_stream<D, BF16, 2>(a, stream); break;
-    case AttnKernel::Stream64:
-      if constexpr (D <= 128) launch_stream<D, BF16, 4>(a, stream);
-      break;
     case AttnKernel::Tiled: {
       const hipError_t t = launch_attention_tiled(a, D, BF16, stream);
       if (t != hipSuccess) return t;
@@ -623,12 +629,9 @@ AttnPlan plan_attention(int64_t heads, int64_t kv_heads, int64_t head_dim, int64
   if (rows <= 16) {
     p.kernel = AttnKernel::Stream16;
     p.rows = 16;
-  } else if (rows <= 32) {
+  } else if (rows <= 192) {
     p.kernel = AttnKernel::Stream32;
     p.rows = 32;
-  } else if (rows <= 64 && head_dim <= 128) {
-    p.kernel = AttnKernel::Stream64;
-    p.rows = 64;
   } else {
     p.kernel = AttnKernel::Tiled;
     p.rows = 256;

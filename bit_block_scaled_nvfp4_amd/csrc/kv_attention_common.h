@@ -432,8 +432,10 @@ struct Share {
         uint64_t n = units - off;
         if (n > end - x) n = end - x;
         segment.r = r;
-        segment.tile = (int32_t)quotient(item, (uint64_t)a.kv_heads);
-        segment.kv_head = (int32_t)(item - (uint64_t)segment.tile * (uint32_t)a.kv_heads);
+        // row tiles of one KV head lie next to each other: neighbouring workers read the same keys
+        const uint32_t tiles = (uint32_t)quotient(total, (uint64_t)units * (uint32_t)a.kv_heads);
+        segment.kv_head = (int32_t)quotient(item, tiles);
+        segment.tile = (int32_t)(item - (uint64_t)segment.kv_head * tiles);
         segment.u0 = (int32_t)off;
         segment.u1 = (int32_t)(off + n);
         segment.first = off == 0;
