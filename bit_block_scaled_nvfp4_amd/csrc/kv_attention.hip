@@ -629,7 +629,7 @@ AttnPlan plan_attention(int64_t heads, int64_t kv_heads, int64_t head_dim, int64
   if (rows <= 16) {
     p.kernel = AttnKernel::Stream16;
     p.rows = 16;
-  } else if (rows <= 192) {
+  } else if (rows <= 96) {
     p.kernel = AttnKernel::Stream32;
     p.rows = 32;
   } else {
@@ -639,7 +639,9 @@ AttnPlan plan_attention(int64_t heads, int64_t kv_heads, int64_t head_dim, int64
   p.join_rows = (int32_t)(rows < p.rows ? rows : p.rows);
   const int64_t items = requests * kv_heads * ((rows + p.rows - 1) / p.rows);
   if (p.kernel == AttnKernel::Tiled) {
-    if (max_seq_len > 256 && items < kComputeUnits) p.workers = kComputeUnits;
+    // where the context is most of the work all row tiles cost alike and sharing balances ragged lengths
+    const bool deep = 4 * max_query_len <= max_seq_len;
+    if (max_seq_len > 256 && items < (deep ? 4 : 1) * kComputeUnits) p.workers = kComputeUnits;
   } else if (max_seq_len > 2 * kUnit && items < 4 * kComputeUnits) {
     p.workers = stream_groups((int)head_dim, p.rows) * kComputeUnits;
   }

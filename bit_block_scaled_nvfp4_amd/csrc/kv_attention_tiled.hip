@@ -14,9 +14,9 @@
 //            in a 16-key step are {4 h .. 4 h + 3} and {8 + 4 h ..}, h = lane / 32, and V^T lies in LDS
 //            with its keys in that order.
 //
-// Two LDS buffers: while tile t is multiplied out of one, tile t + 1 goes from registers into the
-// other, tile t + 2 is on its way from the cache into those registers and the slots of tile t + 3 are
-// looked up; one barrier a tile.
+// Two LDS buffers: while a tile is multiplied out of one, the next goes from registers into the other,
+// the two after it are on their way from the cache into registers (one was not enough to cover a read
+// of HBM) and the slots of the one after those are looked up; one barrier a tile.
 #include "kv_attention_common.h"
 
 namespace nvfp4 {
@@ -347,8 +347,8 @@ struct Shared {
   int32_t limits[kWaves][4];
   int32_t nans[2][kWaves];
   float away[kWaves][kKeys<D>];  // drafted keys' positions less their places
-  int32_t slots[4][128];    // of the tiles t with t % 4 = index
-  uint64_t in_cache[4][2];
+  int32_t slots[8][128];    // of the tiles t with t % 8 = index
+  uint64_t in_cache[8][2];
   Share<kThreads> share;
 };
 
@@ -450,16 +450,16 @@ __device__ __forceinline__ void segment(const Segment& sg, Shared<D>& lds) {
   const auto put_slots = [&](int32_t t) {
     const int32_t x = slot_of(a, e0, hi_max, (uint32_t)t * BN + o0);
     const uint64_t b = __ballot(x >= 0);
-    if (lane < BN) lds.slots[t & 3][o0] = x;
+    if (lane < BN) lds.slots[t & 7][o0] = x;
     uint64_t c1 = ~0ull;
     if constexpr (D == 64) {
       const int32_t y = slot_of(a, e1, hi_max, (uint32_t)t * BN + o1);
       c1 = __ballot(y >= 0);
-      lds.slots[t & 3][o1] = y;
+      lds.slots[t & 7][o1] = y;
     }
     if (lane == 0) {
-      lds.in_cache[t & 3][0] = b;
-      lds.in_cache[t & 3][1] = c1;
+      lds.in_cache[t & 7][0] = b;
+      lds.in_cache[t & 7][1] = c1;
     }
   };
   // from the last tile to the first: what is nearest, and with a distance bias weighs most, comes first
@@ -469,29 +469,36 @@ __device__ __forceinline__ void segment(const Segment& sg, Shared<D>& lds) {
     There<D> cur, nxt;
     // whether every row of the workgroup sees all of tile t
     const auto whole = [&](int32_t t, const There<D>& th) { return th.all() && t * BN >= lo_all && (t + 1) * BN <= hi_all; };
-    // the first three tiles by one wavefront each, and the first entries of the loop's own look-ups
+    // the first four tiles by one wavefront each, and the first entries of the loop's own look-ups
     const int32_t te = t1 - 1;
-    load_entries(te - (wave < 3 ? wave : 3));
-    if (wave < 3) put_slots(te - wave);
+    load_entries(te - (wave < 4 ? wave : 4));
+    if (wave < 4) put_slots(te - wave);
     lds_barrier();
-    fetch<D>(a, lds.slots[te & 3], lds.in_cache[te & 3], kbase, vbase, tid, f, cur);
-    const bool bad = stage<D, BF16>(f, cur, whole(te, cur), lds.tiles[0][0], lds.tiles[0][1], tid);
+    Fetched f0;
+    There<D> nx2;
+    fetch<D>(a, lds.slots[te & 7], lds.in_cache[te & 7], kbase, vbase, tid, f0, cur);
+    fetch<D>(a, lds.slots[(te - 1) & 7], lds.in_cache[(te - 1) & 7], kbase, vbase, tid, f, nxt);
+    const bool bad = stage<D, BF16>(f0, cur, whole(te, cur), lds.tiles[0][0], lds.tiles[0][1], tid);
     if (lane == 0) lds.nans[0][wave] = bad;
-    fetch<D>(a, lds.slots[(te - 1) & 3], lds.in_cache[(te - 1) & 3], kbase, vbase, tid, f, nxt);
+    fetch<D>(a, lds.slots[(te - 2) & 7], lds.in_cache[(te - 2) & 7], kbase, vbase, tid, f0, nx2);
     lds_barrier();
-    for (int32_t t = te; t >= t0; --t) {
-      const int b = (te - t) & 1;
+    // Turn of tile t out of buffer b: `x` holds the codes of tile t - 1, and then takes those of t - 3.
+    const auto turn = [&](int32_t t, int b, Fetched& x) {
       // LDS and cache offsets are formed anew in each turn (a few instructions): kept in registers
       // through the loop, they push operands out to scratch memory
-      if constexpr (D == 256) asm volatile("" : "+v"(tid));
-      There<D> after = nxt;
+      if constexpr (D != 128) asm volatile("" : "+v"(tid));
+      There<D> after = nx2;
       if (t > t0) {
-        const bool bad2 = stage<D, BF16>(f, nxt, whole(t - 1, nxt), lds.tiles[b ^ 1][0], lds.tiles[b ^ 1][1], tid);
+        const bool bad2 = stage<D, BF16>(x, nxt, whole(t - 1, nxt), lds.tiles[b ^ 1][0], lds.tiles[b ^ 1][1], tid);
         if (lane == 0) lds.nans[b ^ 1][wave] = bad2;
-        if (wave == kLookUp + (t & 3)) put_slots(t - 3);
-        // tiles before the first have negative positions, which have no slot: they read slot 0 and are not used
-        fetch<D>(a, lds.slots[(t - 2) & 3], lds.in_cache[(t - 2) & 3], kbase, vbase, tid, f, after);
-        if (wave == kLookUp + ((t - 1) & 3)) load_entries(t - 4);
+        if (wave == kLookUp + (t & 3)) put_slots(t - 4);
+        // (ahead of the codes: loads land in order, and an entry requested after them would be waited for
+        // with them)
+        if (wave == kLookUp + ((t - 1) & 3)) load_entries(t - 5);
+        __builtin_amdgcn_sched_barrier(0);
+        // tiles before the first have negative positions, which have no slot: they read slot 0 and are
+        // not used
+        fetch<D>(a, lds.slots[(t - 3) & 7], lds.in_cache[(t - 3) & 7], kbase, vbase, tid, x, after);
       }
       const int32_t j0 = t * BN;
       if (j0 < s.hi_max && j0 + BN > s.lo_min) {
@@ -503,8 +510,15 @@ __device__ __forceinline__ void segment(const Segment& sg, Shared<D>& lds) {
         multiply<D, BF16, MODS>(a.cap, rq, qt, lds.tiles[b][0], lds.tiles[b][1], cur, uniform(nans) != 0, moved, lds.away[wave], lds.share.segment, my_row, j0, c, inv_cap, lane, s);
       }
       cur = nxt;
-      nxt = after;
+      nxt = nx2;
+      nx2 = after;
       lds_barrier();
+    };
+    for (int32_t t = te;; t -= 2) {
+      turn(t, 0, f);
+      if (t - 1 < t0) break;
+      turn(t - 1, 1, f0);
+      if (t - 2 < t0) break;
     }
   }
 
