@@ -33,43 +33,44 @@ constexpr int kLookUp = 4;  // wavefronts 4 .. 7 look up slots in turn
 template <int D>
 constexpr int kKeys = 8192 / D;  // positions of a tile: 32, 64, 128
 
-// LDS layouts.  A 16-byte access is served to lanes {4 k .. 4 k + 3} of both halves of a wavefront (or to
-// 8 neighbours) at a time, from 8 columns of 16 bytes; column numbers are scrambled so that such
-// lanes, reading one granule (lane half: two neighbouring ones) of 4 or 8 neighbouring keys or dims,
-// touch 8 different columns, and so do the stores.
+// LDS layouts.  Tiles are rows of 256 bytes, 16 columns of 16; the column number is scrambled (an exclusive
+// or that depends on the key or dim) so that 16 neighbouring lanes, or 8 of each half of a wavefront,
+// reading one granule (lane half: two neighbouring ones) of as many neighbouring keys or dims, touch 16
+// different columns, and so do the stores.  With 8 columns scrambled an operand read took 12 clocks
+// instead of 8.
 
 // Byte offset of granule `gr` (8 dims) of key `key` in a K tile [key][D].
 template <int D>
 __device__ __forceinline__ int k_offset(int key, int gr) {
-  const int f = (key & 2) | ((key >> 2) & 1) | ((key & 1) << 2);
-  return key * (2 * D) + ((gr ^ f) << 4);
+  const int k0 = key & 1, k1 = (key >> 1) & 1, k2 = (key >> 2) & 1, k3 = (key >> 3) & 1;
+  if constexpr (D == 64)  // two keys a row
+    return ((key >> 1) << 8) + ((((k0 << 3) | gr) ^ ((k1 << 2) | (k2 << 1) | k3)) << 4);
+  return key * (2 * D) + ((gr ^ ((k0 << 3) | (k1 << 2) | (k2 << 1) | k3)) << 4);
 }
 
-// Byte offset of granule `gr` (8 keys) of dim `dim` in a V^T tile [dim][keys].  Stores write half
-// granules: 4 dims that lie 4 apart, 4 quads of keys.
+// Byte offset of granule `gr` (8 keys) of dim `dim` in a V^T tile [dim][keys]; 1, 2 or 4 dims a row.  Stores
+// write half granules: 8 dims that lie 4 apart, 4 quads of keys.
 template <int D>
 __device__ __forceinline__ int v_offset(int dim, int gr) {
-  const int d0 = dim & 1, d1 = (dim >> 1) & 1, d2 = (dim >> 2) & 1, d3 = (dim >> 3) & 1;
-  if constexpr (D == 256) {
-    // rows of 64 bytes, two to the 8 columns
-    const int f = d2 | ((d1 ^ d2) << 1) | (d3 << 2);
-    return ((dim >> 1) << 7) + ((((d0 << 2) | gr) ^ f) << 4);
-  } else {
-    const int f = d2 | ((d0 ^ d2) << 1) | ((d1 ^ d3) << 2);
-    return dim * (2 * kKeys<D>) + ((gr ^ f) << 4);
-  }
+  const int d0 = dim & 1, d1 = (dim >> 1) & 1, d2 = (dim >> 2) & 1, d3 = (dim >> 3) & 1, d4 = (dim >> 4) & 1;
+  if constexpr (D == 256)
+    return ((dim >> 2) << 8) + ((((d1 << 3) | (d0 << 2) | gr) ^ ((d4 << 3) | (d3 << 2) | (d2 << 1) | d3)) << 4);
+  if constexpr (D == 128)
+    return ((dim >> 1) << 8) + ((((d0 << 3) | gr) ^ ((d4 << 3) | (d2 << 2) | ((d1 ^ d3) << 1) | d3)) << 4);
+  return (dim << 8) + ((gr ^ (((d0 ^ d4) << 3) | ((d1 ^ d3) << 2) | (d2 << 1) | d3)) << 4);
 }
 
-// What a lane reads of those tiles, granule 2 e + h of key or dim 32 n + r: the scramble depends on r
-// alone, so four addresses and constant offsets serve all e and n.
+// What a lane reads of those tiles, granule 2 e + h of key or dim 32 n + r, from its offset for e = n = 0:
+// the scramble depends on r alone, so e's low bits are exchanged into the column and the rest is a
+// constant offset.
 template <int D>
-__device__ __forceinline__ u32x4 read_k(const char* const (&kp)[4], int n, int e) {
-  return *reinterpret_cast<const u32x4*>(kp[e & 3] + n * (64 * D) + (e >> 2) * 128);
+__device__ __forceinline__ u32x4 read_k(const char* tile, int at, int n, int e) {
+  return *reinterpret_cast<const u32x4*>(tile + (at ^ ((e & 7) << 5)) + n * (64 * D) + (e >> 3) * 256);
 }
 
 template <int D>
-__device__ __forceinline__ u32x4 read_v(const char* const (&vp)[4], int n, int e) {
-  return *reinterpret_cast<const u32x4*>(vp[e & 3] + n * (64 * kKeys<D>) + (e >> 2) * 128);
+__device__ __forceinline__ u32x4 read_v(const char* tile, int at, int n, int e) {
+  return *reinterpret_cast<const u32x4*>(tile + (at ^ (e << 5)) + n * (64 * kKeys<D>));
 }
 
 template <bool BF16>
@@ -218,12 +219,7 @@ __device__ __forceinline__ void multiply(float cap, const Request& rq, const cha
                                          bool nans, bool moved, float* away, const Segment& now, uint32_t my_row, int32_t j0, float c, float inv_cap, int lane, WaveState<D>& s) {
   constexpr int N = kKeys<D> / 32;
   const int r = lane & 31, h = lane >> 5;
-  const char *kp[4], *vp[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    kp[e] = kt + k_offset<D>(r, 2 * e + h);
-    vp[e] = vt + v_offset<D>(r, (2 * e + h) & (kKeys<D> / 8 - 1));
-  }
+  const int kat = k_offset<D>(r, h), vat = v_offset<D>(r, h);
   f32x16 x[N];
 #pragma unroll
   for (int n = 0; n < N; ++n) {
@@ -231,7 +227,7 @@ __device__ __forceinline__ void multiply(float cap, const Request& rq, const cha
     for (int i = 0; i < 16; ++i) x[n][i] = 0.0f;
 #pragma unroll
     for (int e = 0; e < D / 16; ++e)
-      x[n] = mfma32<BF16>(read_k<D>(kp, n, e), e < kQueryRegs<D> ? s.q[e < kQueryRegs<D> ? e : 0] : *reinterpret_cast<const u32x4*>(qt + (e - kQueryRegs<D>) * 1024), x[n]);
+      x[n] = mfma32<BF16>(read_k<D>(kt, kat, n, e), e < kQueryRegs<D> ? s.q[e < kQueryRegs<D> ? e : 0] : *reinterpret_cast<const u32x4*>(qt + (e - kQueryRegs<D>) * 1024), x[n]);
   }
   // the phases' instructions stay apart: mixed, they need more registers than there are
   __builtin_amdgcn_sched_barrier(0);
@@ -313,7 +309,7 @@ __device__ __forceinline__ void multiply(float cap, const Request& rq, const cha
   for (int d = 0; d < D / 32; ++d)
 #pragma unroll
     for (int e = 0; e < 2 * N; ++e)
-      s.acc[d] = mfma32<false>(read_v<D>(vp, d, e), p[e], s.acc[d]);
+      s.acc[d] = mfma32<false>(read_v<D>(vt, vat, d, e), p[e], s.acc[d]);
   if (rarely(nans)) {
     // NaN codes among the tile's values were staged as zeros, so that they cannot reach rows that do not
     // see them; the rows that do are set here, from the cache
