@@ -9,6 +9,7 @@ the current stream of the tensors' device; PyTorch provides device memory.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import bit_block_scaled_nvfp4_amd as _base
 
@@ -166,6 +167,12 @@ def _rows(t, shape, dtype, device, name):
     return (ts if shape[0] > 1 else shape[1] * shape[2]), (hs if shape[1] > 1 else shape[2])
 
 
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(*sizes):
+    """Workspace of a call of these sizes (a function of them alone)."""
+    return _lib().nvfp4_kv_fp8_attention_workspace(*sizes)
+
+
 def _attention(fn_name, q, key_cache, value_cache, key_scale, value_scale, block_table, query_start,
                seq_lens, block_size, num_kv_heads, scale, softcap, slopes, extra, max_query_len,
                max_seq_len, out):
@@ -216,7 +223,7 @@ def _attention(fn_name, q, key_cache, value_cache, key_scale, value_scale, block
     W = block_table.shape[1]
     max_query_len = max(1, T if max_query_len is None else int(max_query_len))
     max_seq_len = max(1, min(W * block_size, 2**31 - 1) if max_seq_len is None else int(max_seq_len))
-    need = lib.nvfp4_kv_fp8_attention_workspace(T, H, num_kv_heads, D, R, max_query_len, max_seq_len)
+    need = _workspace_bytes(T, H, num_kv_heads, D, R, max_query_len, max_seq_len)
     # from the caching allocator on the current stream: no two calls that may run at once share one
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     _call(dev, getattr(lib, fn_name), q.data_ptr(), _base.NVFP4_BF16 if q.dtype == torch.bfloat16 else _base.NVFP4_F16,

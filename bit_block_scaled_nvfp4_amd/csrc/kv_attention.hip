@@ -29,6 +29,7 @@ constexpr int kThreads = 256;
 constexpr int kWaves = 4;
 constexpr int kStep = 32;              // positions of a wavefront's step
 constexpr int kUnit = kWaves * kStep;  // positions of a workgroup's step
+constexpr int kShort = 8 * kUnit;      // positions that a workgroup walks over alone
 
 // Workgroups that share a compute unit's registers: what a call is divided among.  More of them keep more
 // loads in flight, as long as their operands fit: 4 KB a step and wavefront with 64 dims, 16 KB with 256.
@@ -626,10 +627,19 @@ AttnPlan plan_attention(int64_t heads, int64_t kv_heads, int64_t head_dim, int64
                         int64_t max_query_len, int64_t max_seq_len) {
   AttnPlan p{};
   const int64_t rows = max_query_len * (heads / kv_heads);
+  // Short sequences: one launch of a workgroup per item and no join (one token over 500 positions, 256
+  // dims: 16 us a call; shared among workers and joined 20 us), by row tiles of 32 where these all run
+  // at once (37-token prompt, 222 rows: 15 us; tiles of 256 rows 19 us.  64 prompts of 60 tokens, which
+  // do not run at once: 30 us against 18 us).
+  const bool small = max_seq_len <= kShort && requests * kv_heads * ((rows + 31) / 32) <= kComputeUnits;
   if (rows <= 16) {
     p.kernel = AttnKernel::Stream16;
     p.rows = 16;
-  } else if (rows <= 96) {
+  } else if (rows <= 96 || small) {
+    // tiles of 32 rows re-read the keys from the caches and decode them again; tiles of 256 leave
+    // wavefronts idle (64 requests x 6001 positions: 96 rows of 256 dims 277 us against 317 us, 48 rows
+    // of 128 dims 219 us against 290 us; 192 rows of 128 dims 553 us against 364 us, 128 rows of 64
+    // dims 287 us against 184 us)
     p.kernel = AttnKernel::Stream32;
     p.rows = 32;
   } else {
@@ -639,10 +649,12 @@ AttnPlan plan_attention(int64_t heads, int64_t kv_heads, int64_t head_dim, int64
   p.join_rows = (int32_t)(rows < p.rows ? rows : p.rows);
   const int64_t items = requests * kv_heads * ((rows + p.rows - 1) / p.rows);
   if (p.kernel == AttnKernel::Tiled) {
-    // where the context is most of the work all row tiles cost alike and sharing balances ragged lengths
+    // Where the context is most of the work all row tiles cost alike and sharing balances ragged
+    // lengths (64 trees of 192 rows: 355 us; a workgroup per item 386 us).  A prompt's row tiles cost
+    // as much as they see: they are shared only where they are too few to occupy the device.
     const bool deep = 4 * max_query_len <= max_seq_len;
     if (max_seq_len > 256 && items < (deep ? 4 : 1) * kComputeUnits) p.workers = kComputeUnits;
-  } else if (max_seq_len > 2 * kUnit && items < 4 * kComputeUnits) {
+  } else if (max_seq_len > kShort && items < 4 * kComputeUnits) {
     p.workers = stream_groups((int)head_dim, p.rows) * kComputeUnits;
   }
   if (p.workers)
