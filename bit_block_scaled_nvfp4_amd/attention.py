@@ -221,7 +221,8 @@ def _attention(fn_name, q, key_cache, value_cache, key_scale, value_scale, block
     else:
         out_ts, out_hs = _rows(out, (T, H, D), q.dtype, dev, "out")
     W = block_table.shape[1]
-    max_query_len = max(1, T if max_query_len is None else int(max_query_len))
+    # without a word from the caller: every request has one token at least
+    max_query_len = max(1, T - R + 1 if max_query_len is None else int(max_query_len))
     max_seq_len = max(1, min(W * block_size, 2**31 - 1) if max_seq_len is None else int(max_seq_len))
     need = _workspace_bytes(T, H, num_kv_heads, D, R, max_query_len, max_seq_len)
     # from the caching allocator on the current stream: no two calls that may run at once share one

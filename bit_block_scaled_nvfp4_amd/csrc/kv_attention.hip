@@ -331,7 +331,7 @@ __device__ __forceinline__ void segment(const Segment& sg, bool split, int32_t w
     if (w.token >= 0) {
       // a tree's rows see at most the request's keys, and below ctx all of them
       lo_min = min(lo_min, w.lo);
-      hi_max = max(hi_max, a.tree ? rq.len : w.hi);
+      hi_max = max(hi_max, a.tree ? rq.keys : w.hi);
       lo_max = max(lo_max, w.lo);
       hi_min = min(hi_min, w.hi);
     }
@@ -347,7 +347,6 @@ __device__ __forceinline__ void segment(const Segment& sg, bool split, int32_t w
   s.hi_all = __builtin_amdgcn_readfirstlane(hi_min);
   lo_min = __builtin_amdgcn_readfirstlane(lo_min);
   hi_max = __builtin_amdgcn_readfirstlane(hi_max);
-  if (hi_max > rq.len) hi_max = rq.len;
   int32_t u0 = sg.u0, u1 = sg.u1;
   if (lo_min >= hi_max) {
     u1 = u0;
@@ -480,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, stream_groups(D, 16 * NQ)) attention
     s.last_worker = 0;
     const Request q = request_of(a, s.r);
     s.u0 = 0;
-    s.u1 = (int32_t)(((uint32_t)q.len + kUnit - 1) / kUnit);
+    s.u1 = (int32_t)(((uint32_t)q.keys + kUnit - 1) / kUnit);
     const int32_t tiles = (int32_t)(((uint32_t)q.count * a.group.d + kRows - 1) / kRows);
     for (s.tile = blockIdx.z; s.tile < tiles; s.tile += gridDim.z) segment<D, BF16, NQ, MODS>(s, false, 0, lds);
     return;

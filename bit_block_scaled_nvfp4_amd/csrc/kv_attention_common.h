@@ -74,7 +74,8 @@ struct Row {
 
 struct Request {
   int32_t start, count;  // query rows
-  int32_t len, ctx;      // positions in the cache; len - count
+  int32_t len, ctx;      // positions of the request; len - count
+  int32_t keys;          // of them, as many as the block table has columns for
 };
 
 __device__ __forceinline__ Request request_of(const AttnArgs& a, int32_t r) {
@@ -87,6 +88,8 @@ __device__ __forceinline__ Request request_of(const AttnArgs& a, int32_t r) {
   const int32_t l = a.seq_lens[r];
   q.len = l > 0 ? l : 0;
   q.ctx = q.len - q.count;
+  const int64_t room = (int64_t)a.table_width * a.bs.d;
+  q.keys = q.len < room ? q.len : (int32_t)room;
   return q;
 }
 
@@ -113,7 +116,7 @@ __device__ __forceinline__ Row row_of(const AttnArgs& a, int32_t r, const Reques
   w.pos = q.ctx + (w.token - q.start);
   if (a.slopes) w.slope = a.slopes[w.head] * kLog2e;
   if (a.tree) {
-    w.hi = q.ctx > 0 ? q.ctx : 0;
+    w.hi = q.ctx > 0 ? (q.ctx < q.keys ? q.ctx : q.keys) : 0;
     if (a.slopes && a.positions) w.pos = a.positions[w.token];
   } else {
     int32_t end = w.pos + 1;
@@ -121,7 +124,7 @@ __device__ __forceinline__ Row row_of(const AttnArgs& a, int32_t r, const Reques
       const int32_t p = a.prefix_lens[r];
       end = end > p ? end : p;
     }
-    w.hi = end < 0 ? 0 : (end > q.len ? q.len : end);
+    w.hi = end < 0 ? 0 : (end > q.keys ? q.keys : end);
     if (a.doc_start) {
       const int32_t s = a.doc_start[w.token];
       w.lo = s > 0 ? s : 0;
@@ -284,7 +287,7 @@ __device__ __forceinline__ void weight_of(const AttnArgs& a, int32_t r, int32_t 
                                           uint32_t& units, uint64_t& total) {
   const Request q = request_of(a, r);
   const uint64_t tiles = ((uint64_t)q.count * a.group.d + rows - 1) / (uint32_t)rows;
-  units = ((uint32_t)q.len + (uint32_t)unit - 1) / (uint32_t)unit;
+  units = ((uint32_t)q.keys + (uint32_t)unit - 1) / (uint32_t)unit;
   if (units == 0) units = 1;  // the rows still get their zeros
   total = (uint64_t)units * tiles * (uint32_t)a.kv_heads;
 }

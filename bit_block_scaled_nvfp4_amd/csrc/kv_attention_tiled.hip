@@ -390,7 +390,7 @@ __device__ __forceinline__ void segment(const Segment& sg, Shared<D>& lds) {
   int32_t lo_min = 0x7FFFFFFF, hi_max = 0, lo_all = 0, hi_all = 0x7FFFFFFF;
   if (row.token >= 0) {
     lo_min = lo_all = row.lo;
-    hi_max = a.tree ? rq.len : row.hi;
+    hi_max = a.tree ? rq.keys : row.hi;
     hi_all = row.hi;
   }
 #pragma unroll
@@ -401,7 +401,7 @@ __device__ __forceinline__ void segment(const Segment& sg, Shared<D>& lds) {
     hi_all = min(hi_all, __shfl_xor(hi_all, d));
   }
   s.lo_min = __builtin_amdgcn_readfirstlane(lo_min);
-  s.hi_max = min(__builtin_amdgcn_readfirstlane(hi_max), rq.len);
+  s.hi_max = __builtin_amdgcn_readfirstlane(hi_max);
   s.lo_all = __builtin_amdgcn_readfirstlane(lo_all);
   s.hi_all = __builtin_amdgcn_readfirstlane(hi_all);
   if (lane == 0) {
@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(kThreads) attention_tiled_kernel(AttnArgs) {
     s.last_worker = 0;
     const Request q = request_of(a, s.r);
     s.u0 = 0;
-    s.u1 = (int32_t)(((uint32_t)q.len + kKeys<D> - 1) / kKeys<D>);
+    s.u1 = (int32_t)(((uint32_t)q.keys + kKeys<D> - 1) / kKeys<D>);
     const int32_t tiles = (int32_t)(((uint32_t)q.count * a.group.d + kRows - 1) / kRows);
     // the last row tiles see the most keys: they start first
     for (int32_t k = blockIdx.z; k < tiles; k += gridDim.z) {

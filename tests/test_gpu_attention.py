@@ -384,3 +384,72 @@ def test_two_streams_at_once():
         for o in outs[k]:
             assert bool((o == outs[k][0]).all())
         compare(outs[k][0].double().cpu().numpy(), want, tol, f"stream {k}")
+
+
+@pytest.mark.parametrize("split", [False, True])
+@pytest.mark.parametrize("mods", [False, True])
+@pytest.mark.parametrize("new", [1, 9, 40])
+@pytest.mark.parametrize("head_dim", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_every_kernel_and_division(dtype, head_dim, new, mods, split):
+    """4 heads a KV head: 4, 36 and 160 rows, so tiles of 16, 32 and 256; a workgroup per item, and shared
+    among workers and joined; plain scores, and capped and biased ones; prompts and trees."""
+    lens = [(700, new), (33, max(1, new // 2)), (0, new), (300, new)]
+    for tree in (False, True):
+        p = Problem(lens, 8, 2, head_dim, dtype=dtype, seed=50 + new, q_std=2.0)
+        if mods:
+            p.options["softcap"] = 12.0
+            p.options["slopes"] = np.linspace(0.01, 0.7, 8).astype(np.float32)
+        if tree:
+            counts = [n for _, n in lens]
+            p.options["tree_mask"] = tree_mask(p.rng, counts)
+            if mods:
+                p.options["positions"] = np.concatenate([c + p.rng.integers(0, 4, n) for c, n in lens])
+        # a row tile of 256 is shared where the context is most of the work
+        hint = 100000 if split else (1000 if new < 40 else 100)
+        check(p, f"{dtype} D={head_dim} new={new} mods={mods} split={split} tree={tree}", max_query_len=new,
+              max_seq_len=hint)
+
+
+@pytest.mark.parametrize("requests,new", [(300, 2), (700, 1), (600, 60)])
+def test_more_requests_than_threads_share_the_work(requests, new):
+    rng = np.random.default_rng(requests)
+    lens = [(int(rng.integers(0, 60)), int(rng.integers(0, new + 1))) for _ in range(requests)]
+    lens[requests // 2] = (2000, new)
+    p = Problem(lens, 2, 1, 64, seed=5)
+    check(p, f"{requests} requests shared", max_query_len=new, max_seq_len=10 ** 6)
+
+
+def test_lengths_beyond_the_table_end_in_time():
+    """seq_lens far beyond what the table holds (left over from another batch): the keys that the table
+    has are used, positions count from the length given."""
+    p = Problem([(60, 2), (40, 30)], 4, 2, 64, seed=34)
+    p.table = p.table[:, :3].copy()
+    want, tol = p.oracle()
+    huge = p.seq_lens.copy()
+    huge[0] = 2 ** 31 - 1  # every key of the table lies below both rows
+    p.seq_lens = np.array([48 + 2, huge[1]])  # the oracle's loops: the same 48 keys, all of them seen
+    want, tol = p.oracle()
+    d = p.device()
+    import torch
+
+    d["seq_lens"] = torch.tensor([2 ** 31 - 1, int(huge[1])], dtype=torch.int32, device=DEV)
+    for hint in (64, 10 ** 6):
+        log(f"huge length hint={hint}")
+        d["out"].fill_(SENTINEL)
+        compare(p.run(**{**d, "max_seq_len": hint}), want, tol, f"hint {hint}")
+
+
+def test_padding_without_requests():
+    p = Problem([(5, 0), (9, 0)], 4, 2, 64, seed=35, pad_tokens=6)
+    for hint in (64, 10 ** 6):
+        got = check(p, "no tokens", max_seq_len=hint)
+        assert np.all(got == SENTINEL)
+
+
+def test_rows_before_the_first_request_and_default_bounds():
+    """query_start that begins above 0, and no bounds given."""
+    p = Problem([(30, 1)] * 40, 8, 2, 128, seed=36, pad_tokens=3)
+    p.query_start = p.query_start + 2
+    got = check(p, "offset rows")
+    assert np.all(got[:2] == SENTINEL) and np.all(got[42:] == SENTINEL)
