@@ -20,6 +20,13 @@ Entry points (same names as the C ABI):
 * ``nvfp4_harmonize_segments(codes, scales, seg_gscale, seg_offsets)`` -> ``(codes, scales, g)``
 * ``nvfp4_kv_fp8_store(key, value, key_scale, value_scale, key_cache, value_cache, slot_mapping)``
 * ``nvfp4_kv_fp8_load(cache, scale, slot_mapping, out_dtype)`` -> decoded rows
+* ``nvfp4_kv_block_tables(context_lens, query_lens, free_blocks, block_table, block_size, ...)`` ->
+  ``(slot_mapping, positions, query_start, seq_lens, blocks_needed)``
+* ``nvfp4_kv_fp8_attention(q, key_cache, value_cache, key_scale, value_scale, block_table,
+  query_start, seq_lens, block_size=, num_kv_heads=, ...)`` -> attention of prompts and single tokens
+* ``nvfp4_kv_fp8_tree_attention(..., tree_mask, ...)`` -> attention of trees of drafted tokens
+
+The last three (``include/nvfp4_attention.h``) are in ``attention.py``.
 """
 
 from __future__ import annotations

@@ -17,6 +17,12 @@
 // Two LDS buffers: while a tile is multiplied out of one, the next goes from registers into the other,
 // the two after it are on their way from the cache into registers (one was not enough to cover a read
 // of HBM) and the slots of the one after those are looked up; one barrier a tile.
+//
+// Measured (a dense bf16 library product reaches 1.26 PFLOP/s on the same card): 16384-token prompt, 24
+// heads of 256 dims over 4 KV heads, 3.24 ms, 1.02 PFLOP/s; 32 heads of 128 dims 0.98, of 64 dims 0.77,
+// of 128 dims with capped scores 0.78 PFLOP/s.  The matrix cores are busy 44 % of the time at 256 dims; a
+// wavefront's own chain (operand reads, scores, softmax, output) takes as long as two of them share a
+// SIMD, so tiles with half their rows empty take as long as full ones.
 #include "kv_attention_common.h"
 
 namespace nvfp4 {

@@ -8,6 +8,9 @@
 // and of new blocks by binary search in them.  A token in a new block reads the block's number from the
 // free list, not from the table entry that another workgroup may still be writing; entries below
 // `have` are only read and entries from `have` on only written.
+//
+// Measured: 3.5 us on the device for 64 requests with one token each, 5.7 us for 500 requests with 29 thousand
+// tokens; 9.6 and 10.0 us a call from Python, most of it the binding's.
 #include "attention_internal.h"
 
 namespace nvfp4 {
