@@ -251,7 +251,9 @@ def nvfp4_kv_fp8_attention(q, key_cache, value_cache, key_scale, value_scale, bl
     hides the positions before each token's document, ``prefix_lens`` (int32 ``[requests]``) shows each
     request's prefix to all its tokens.  Rows that see nothing are zero; rows of no request are left as
     they were.  ``max_query_len`` and ``max_seq_len`` (bounds of the requests' lengths) only choose how
-    the work is divided.  Returns ``out`` in q's type."""
+    the work is divided.  Single tokens in a call with prompts cost as much as 256 rows each over their
+    context: many of them over long contexts are faster in a call of their own.  Returns ``out`` in q's
+    type."""
     torch = _base._torch()
 
     def extra(T, R, dev):

@@ -105,7 +105,7 @@ nvfp4_status run(const Call& c, const int32_t* doc_start, const int32_t* prefix_
                  const int64_t* tree, int64_t tree_words, int64_t tree_ld,
                  const int32_t* positions, void* stream) {
   const int64_t longest = query_bound(c.max_query_len, c.tokens);
-  const nvfp4::AttnPlan p = nvfp4::plan_attention(c.heads, c.kv_heads, c.head_dim, c.requests, longest, c.max_seq_len);
+  const nvfp4::AttnPlan p = nvfp4::plan_attention(c.tokens, c.heads, c.kv_heads, c.head_dim, c.requests, longest, c.max_seq_len);
   if (p.workspace > 0) {
     if (!c.workspace) return NVFP4_EINVAL;
     if (c.workspace_bytes < p.workspace) return NVFP4_ESHAPE;
@@ -140,8 +140,8 @@ nvfp4_status run(const Call& c, const int32_t* doc_start, const int32_t* prefix_
   a.heads = (int32_t)c.heads;
   a.kv_heads = (int32_t)c.kv_heads;
   const int64_t group = c.heads / c.kv_heads;
-  const int64_t tiles = (longest * group + p.rows - 1) / p.rows;
-  a.row_tiles = (int32_t)(tiles < 4096 ? tiles : 4096);  // (the kernels' strides cover the others)
+  a.row_tiles = p.row_tiles;
+  a.all_tiles = p.all_tiles;
   a.workers = p.workers;
   a.bs = nvfp4::make_fast_div((uint32_t)c.block_size);
   a.group = nvfp4::make_fast_div((uint32_t)group);
@@ -256,7 +256,7 @@ int64_t nvfp4_kv_fp8_attention_workspace(int64_t tokens, int64_t heads, int64_t 
                                          int64_t max_query_len, int64_t max_seq_len) {
   if (!shape_ok(tokens, heads, kv_heads, head_dim, requests, max_query_len, max_seq_len)) return 0;
   if (tokens == 0 || requests == 0) return 0;
-  return nvfp4::plan_attention(heads, kv_heads, head_dim, requests, query_bound(max_query_len, tokens), max_seq_len).workspace;
+  return nvfp4::plan_attention(tokens, heads, kv_heads, head_dim, requests, query_bound(max_query_len, tokens), max_seq_len).workspace;
 }
 
 }  // extern "C"

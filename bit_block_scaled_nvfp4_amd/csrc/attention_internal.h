@@ -54,6 +54,8 @@ struct AttnPlan {
   int32_t join_rows;  // of them, as many as the longest request has
   int32_t workers;  // 0: one workgroup per (row tile, KV head, request); else the number of
                     // workgroups that share the whole key range, and a joining launch
+  int32_t row_tiles;  // of the longest request as far as the caller told (grid bound)
+  int32_t all_tiles;  // > 0 (tiled kernel without workers): the grid counts row tiles of all requests
   int64_t workspace;
 };
 
@@ -82,14 +84,15 @@ struct AttnArgs {
   int32_t* headers;
   int32_t num_slots, table_width, requests, tokens;
   int32_t heads, kv_heads, tree_words;
-  int32_t row_tiles;  // row tiles of the longest request as far as the caller told (grid bound)
-  int32_t workers;
+  int32_t row_tiles, workers;  // as in the plan
   FastDiv bs, group;
   float scale, cap;
+  int32_t all_tiles;  // as in the plan
 };
 
-AttnPlan plan_attention(int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t requests,
-                        int64_t max_query_len, int64_t max_seq_len);
+AttnPlan plan_attention(int64_t tokens, int64_t heads, int64_t kv_heads,
+                        int64_t head_dim, int64_t requests, int64_t max_query_len,
+                        int64_t max_seq_len);
 
 hipError_t launch_block_tables(const TablesArgs& a, hipStream_t stream);
 // Launch the plan's kernel (and, with workers, the joining kernel).

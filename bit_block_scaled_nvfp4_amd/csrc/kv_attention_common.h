@@ -34,6 +34,7 @@ constexpr float kRaise = 4096.0f;
 // Reference of a row that has seen nothing: so far below every score that the first one seen raises it
 // (exp2 overflows to infinity), and finite, so that exp2(-inf - m) is 0 and not NaN.
 constexpr float kNoScore = -1e37f;
+constexpr uint32_t kMinusInf = 0xFF800000u, kPlusInf = 0x7F800000u;
 
 __device__ __forceinline__ uint32_t div_of(uint32_t n, const FastDiv& f) {
   return (uint32_t)(((uint64_t)n * f.mul) >> f.shift);
@@ -157,8 +158,8 @@ __device__ __forceinline__ uint64_t sees64(int32_t lo, int32_t hi, int32_t token
   return bits;
 }
 
-// x where bit b of `seen` is set, else the value with bits `none`, an infinity.  (In integer arithmetic: a tile's selections by condition
-// would hold as many lane masks in scalar registers.)
+// x where bit b of `seen` is set, else the value with bits `none`, an infinity.  (In integer arithmetic: a
+// tile's selections by condition would hold as many lane masks in scalar registers.)
 __device__ __forceinline__ float kept(float x, uint32_t seen, int b, uint32_t none) {
   const uint32_t m = (uint32_t)((int32_t)(seen << (31 - b)) >> 31);
   return __uint_as_float((__float_as_uint(x) & m) | (~m & none));
@@ -314,8 +315,6 @@ __device__ __forceinline__ uint32_t worker_of(uint32_t b, uint32_t P) {
 // after another.  Every workgroup finds its own start by summing the requests' weights (one pass over
 // the lengths, or two where there are more requests than threads), with no launch before it and
 // nothing kept.  The state lies in LDS and the first thread advances it: it is used once a segment.
-constexpr uint32_t kMinusInf = 0xFF800000u, kPlusInf = 0x7F800000u;
-
 template <int NT>
 struct Share {
   uint64_t W, x, end;  // all units; the next unit and the end of this worker's share
@@ -413,6 +412,47 @@ struct Share {
     }
   }
 
+  __device__ __forceinline__ bool take(Segment& s) const {
+    if (!uniform(more)) return false;
+    s.r = uniform(segment.r);
+    s.tile = uniform(segment.tile);
+    s.kv_head = uniform(segment.kv_head);
+    s.u0 = uniform(segment.u0);
+    s.u1 = uniform(segment.u1);
+    s.first = uniform(segment.first);
+    s.last = uniform(segment.last);
+    s.last_worker = uniform(segment.last_worker);
+    return true;
+  }
+
+  // Without sharing: row tile number `worker` of all requests' (of one KV head; a request's last tile first:
+  // it sees the most keys), and the grid's height further at the next call.  False past the last.
+  // Uniform over the workgroup, which has to pass a barrier before the first call and between two.
+  __device__ __forceinline__ bool next_tile(int32_t rows, int32_t unit, Segment& s) {
+    const AttnArgs& a = args();
+    const int tid = threadIdx.x;
+    const int R = a.requests;
+    const uint64_t y = (uint32_t)uniform(worker);
+    if (tid == 0) more = false;
+    uint64_t sum = 0;
+    for (int b = 0; b < R && sum <= y; b += NT) {
+      const int i = b + tid;
+      uint64_t t = i < R ? ((uint64_t)request_of(a, i).count * a.group.d + rows - 1) / (uint32_t)rows : 0, before, all;
+      const uint64_t own = t;
+      scan(t, before, all);
+      const uint64_t first = sum + before + t - own;
+      if (first <= y && y < first + own) {
+        const uint32_t keys = (uint32_t)request_of(a, i).keys;
+        segment = Segment{i, (int32_t)(first + own - 1 - y), (int32_t)blockIdx.x, 0, (int32_t)((keys + (uint32_t)unit - 1) / (uint32_t)unit), true, true, 0};
+        more = true;
+      }
+      sum += all;
+    }
+    if (tid == 0) worker = (int32_t)y + a.all_tiles;  // (behind a barrier of the sums; read again a call later)
+    __syncthreads();
+    return take(s);
+  }
+
   // The next segment, or false when the share is done.  Uniform over the workgroup, which has to pass
   // a barrier between two calls.
   __device__ __forceinline__ bool next(int32_t rows, int32_t unit, Segment& s) {
@@ -450,16 +490,7 @@ struct Share {
       }
     }
     __syncthreads();
-    if (!uniform(more)) return false;
-    s.r = uniform(segment.r);
-    s.tile = uniform(segment.tile);
-    s.kv_head = uniform(segment.kv_head);
-    s.u0 = uniform(segment.u0);
-    s.u1 = uniform(segment.u1);
-    s.first = uniform(segment.first);
-    s.last = uniform(segment.last);
-    s.last_worker = uniform(segment.last_worker);
-    return true;
+    return take(s);
   }
 };
 

@@ -554,12 +554,17 @@ __device__ __forceinline__ void segment(const Segment& sg, Shared<D>& lds) {
   __syncthreads();  // the next segment writes the limits and the tiles again
 }
 
-// MODS: scores are capped or biased.  SPLIT: the workgroups share the items' keys; else each takes whole items.
-template <int D, bool BF16, bool MODS, bool SPLIT>
+// How a workgroup finds its work: the row tile that its place in the grid says; a row tile among all
+// requests' (next_tile); a share of all items' keys.  Three kernels, since what one of them needs beside
+// segment() costs the others registers.
+enum class Work { Place, Search, Share };
+
+// MODS: scores are capped or biased.
+template <int D, bool BF16, bool MODS, Work WORK>
 __global__ void __launch_bounds__(kThreads) attention_tiled_kernel(AttnArgs) {
   __shared__ __align__(16) Shared<D> lds;
   Segment s;
-  if constexpr (!SPLIT) {
+  if constexpr (WORK == Work::Place) {
     const AttnArgs& a = args();
     s.kv_head = blockIdx.x;
     s.r = blockIdx.y;
@@ -575,6 +580,10 @@ __global__ void __launch_bounds__(kThreads) attention_tiled_kernel(AttnArgs) {
       if (threadIdx.x == 0) lds.share.segment = s;  // read again behind segment()'s first barrier
       segment<D, BF16, MODS, false>(s, lds);
     }
+  } else if constexpr (WORK == Work::Search) {
+    if (threadIdx.x == 0) lds.share.worker = blockIdx.y;
+    __syncthreads();
+    while (lds.share.next_tile(kRows, kKeys<D>, s)) segment<D, BF16, MODS, false>(s, lds);
   } else {
     lds.share.begin(kRows, kKeys<D>);
     Header* header = reinterpret_cast<Header*>(args().headers) + blockIdx.x;
@@ -588,12 +597,14 @@ __global__ void __launch_bounds__(kThreads) attention_tiled_kernel(AttnArgs) {
 
 template <int D, bool BF16, bool MODS>
 void launch(const AttnArgs& a, hipStream_t stream) {
-  if (a.workers) {
-    hipLaunchKernelGGL((attention_tiled_kernel<D, BF16, MODS, true>), dim3((uint32_t)a.workers), dim3(kThreads), 0, stream, a);
-  } else {
-    const dim3 grid((uint32_t)a.kv_heads, (uint32_t)a.requests, (uint32_t)a.row_tiles);
-    hipLaunchKernelGGL((attention_tiled_kernel<D, BF16, MODS, false>), grid, dim3(kThreads), 0, stream, a);
-  }
+  const dim3 threads(kThreads), workers((uint32_t)a.workers), search((uint32_t)a.kv_heads, (uint32_t)a.all_tiles);
+  const dim3 place((uint32_t)a.kv_heads, (uint32_t)a.requests, (uint32_t)a.row_tiles);
+  if (a.workers)
+    hipLaunchKernelGGL((attention_tiled_kernel<D, BF16, MODS, Work::Share>), workers, threads, 0, stream, a);
+  else if (a.all_tiles)
+    hipLaunchKernelGGL((attention_tiled_kernel<D, BF16, MODS, Work::Search>), search, threads, 0, stream, a);
+  else
+    hipLaunchKernelGGL((attention_tiled_kernel<D, BF16, MODS, Work::Place>), place, threads, 0, stream, a);
 }
 
 template <int D>

@@ -96,8 +96,9 @@ nvfp4_status nvfp4_kv_block_tables(const int32_t* context_lens, const int32_t* q
  *
  * Arithmetic: q . K is formed by MFMA with exact FP32 products of the query type and the decoded
  * codes, FP32 sums, FP32 scores and softmax statistics; exp(x - reference) is rounded once to FP16
- * (2^-12 relative) for the product with the decoded values, summed in FP32; the result is rounded
- * once to the query type.
+ * (by at most 2^-11 relative, or 2^-25 absolute below 2^-14) for the product with the decoded values,
+ * summed in FP32; the result is rounded once to the query type.  The reference is one of the row's
+ * scores.  Scores (times log2(e)) of -1e37 and less count as -infinity.
  *
  *   q             device, [tokens, heads, head_dim] of dtype (BF16 or F16), token and head strides in
  *                 elements (multiples of 8; head_dim contiguous); 16-byte aligned.
@@ -117,7 +118,11 @@ nvfp4_status nvfp4_kv_block_tables(const int32_t* context_lens, const int32_t* q
  *   out           device, as q; may not overlap q.
  *   workspace     device, 16-byte aligned, at least the bytes that nvfp4_kv_fp8_attention_workspace
  *                 gives for the same arguments; its contents are used within the call only.  Calls
- *                 that may run at the same time need one each.
+ *                 that may run at the same time need one each.  May be NULL where that gives 0.
+ * Single tokens take part in the row tiles of 256 that a prompt in the same call asks for, and cost as
+ * much as a tile full of rows: many of them over long contexts are faster in a call of their own.
+ * Errors: EINVAL (NULL, dtype, scale or softcap not as above), ESHAPE (sizes, strides that let output
+ * elements overlap, a workspace too small), EALIGN.  tokens == 0 or requests == 0 launches nothing.
  */
 nvfp4_status nvfp4_kv_fp8_attention(
     const void* q, nvfp4_dtype dtype, int64_t tokens, int64_t heads, int64_t kv_heads,

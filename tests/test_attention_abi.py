@@ -229,7 +229,7 @@ def test_host_layer_under_address_and_ub_sanitizers(tmp_path):
     stubs.write_text('''
 #include "attention_internal.h"
 namespace nvfp4 {
-AttnPlan plan_attention(int64_t, int64_t, int64_t head_dim, int64_t, int64_t, int64_t max_seq_len) {
+AttnPlan plan_attention(int64_t, int64_t, int64_t, int64_t head_dim, int64_t, int64_t, int64_t max_seq_len) {
   AttnPlan p{};
   p.rows = 16;
   p.workers = max_seq_len > 1024 ? 256 : 0;

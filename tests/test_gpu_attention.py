@@ -453,3 +453,19 @@ def test_rows_before_the_first_request_and_default_bounds():
     p.query_start = p.query_start + 2
     got = check(p, "offset rows")
     assert np.all(got[:2] == SENTINEL) and np.all(got[42:] == SENTINEL)
+
+
+@pytest.mark.parametrize("requests,longest,hint", [(60, 300, 300), (700, 300, 300), (60, 700, 300), (200, 290, 100000)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("head_dim", [64, 128, 256])
+@pytest.mark.parametrize("mods", [False, True])
+def test_one_prompt_among_single_tokens(requests, longest, hint, dtype, head_dim, mods):
+    """Few of the row tiles that the longest request's bound allows exist: workgroups find theirs from
+    the lengths.  First, in the middle and last; bounds below and above the truth."""
+    for place in (0, requests // 2, requests - 1):
+        lens = [((i * 7) % 40, i % 3 % 2) for i in range(requests)]
+        lens[place] = (11, longest)
+        p = Problem(lens, 4, 2, head_dim, dtype=dtype, seed=place + longest, pad_tokens=3)
+        if mods:
+            p.options["softcap"] = 20.0
+        check(p, f"{requests} requests, one of {longest} at {place}, D={head_dim}", max_query_len=hint, max_seq_len=256)
