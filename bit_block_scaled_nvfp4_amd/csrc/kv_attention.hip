@@ -22,9 +22,9 @@
 // load in flight.
 //
 // Measured (HBM reads at 6.4 TB/s in a plain read kernel, copies at 4.9 TB/s): 64 requests x up to 8000
-// positions, one token each, 4 KV heads x 256 dims, 569 MB: 112 us a call, 5.1 TB/s; 128 dims 119 us; 64
-// dims (569 MB counted as 285) 92 us, where the 64-byte pieces of a row and the softmax cost as much as
-// the reads.  One request of 100000 positions, 205 MB: 50 us, of which joining takes 7.
+// positions, one token each, 4 KV heads x 256 dims, 569 MB: 112 us a call, 5.1 TB/s; 8 KV heads x 128
+// dims, 569 MB: 119 us; 8 x 64 dims, 285 MB: 92 us, 3.1 TB/s.  One request of 100000 positions, 205 MB:
+// 50 us, of which joining takes 7.
 #include "kv_attention_common.h"
 
 namespace nvfp4 {

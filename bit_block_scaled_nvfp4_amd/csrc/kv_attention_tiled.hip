@@ -1,7 +1,7 @@
 // Attention of many query rows over the paged FP8 cache: prompts, long chunks, wide drafted trees.
 //
 // What bounds it: the matrix cores, 4 FLOP per query row, visible position and dim, and next to them
-// the vector unit, which spends about 8 instructions a score on the softmax.  A workgroup of 8
+// the vector unit, with about 11 instructions a score (256 dims; staging and addresses included).  A workgroup of 8
 // wavefronts takes 256 query rows, 32 a wavefront, and walks over the keys in tiles of 8192 / head_dim
 // positions (16 KB of keys and 16 KB of values in 16 bits), so a tile costs every wavefront 16 MFMAs of
 // 32 x 32 x 16 for the scores and 16 for the output whatever the head size, and the 32 operand reads
@@ -19,10 +19,11 @@
 // of HBM) and the slots of the one after those are looked up; one barrier a tile.
 //
 // Measured (a dense bf16 library product reaches 1.26 PFLOP/s on the same card): 16384-token prompt, 24
-// heads of 256 dims over 4 KV heads, 3.24 ms, 1.02 PFLOP/s; 32 heads of 128 dims 0.98, of 64 dims 0.77,
-// of 128 dims with capped scores 0.78 PFLOP/s.  The matrix cores are busy 44 % of the time at 256 dims; a
-// wavefront's own chain (operand reads, scores, softmax, output) takes as long as two of them share a
-// SIMD, so tiles with half their rows empty take as long as full ones.
+// heads of 256 dims over 4 KV heads, 3.24 ms, 1.02 PFLOP/s (3.54 ms on a card whose product reaches 1.20);
+// 32 heads of 128 dims 0.99, of 64 dims 0.77, of 128 dims with capped scores 0.79 PFLOP/s.  The matrix
+// cores are busy 45 % of the time at 256 dims, LDS has no bank conflicts.  Tiles with half their rows
+// empty take as long as full ones: with one wavefront a SIMD its own chain (operand reads, scores,
+// softmax, output) shows in full.
 #include "kv_attention_common.h"
 
 namespace nvfp4 {
