@@ -10,6 +10,7 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 constexpr int64_t kMaxI32 = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxSpan = int64_t(1) << 40;
+constexpr int64_t kMaxPositions = kMaxI32 - 255;  // of a request that an attention looks at
 constexpr int64_t kMaxBlockSize = int64_t(1) << 24;
 
 nvfp4_status device_status(hipError_t e) { return e == hipSuccess ? NVFP4_OK : NVFP4_EDEVICE; }
@@ -134,7 +135,9 @@ nvfp4_status run(const Call& c, const int32_t* doc_start, const int32_t* prefix_
   a.tree_words = (int32_t)tree_words;
   a.positions = positions;
   a.num_slots = (int32_t)c.num_slots;
-  a.table_width = (int32_t)c.table_width;
+  // the end of a tile of keys has to stay below 2^31
+  const int64_t columns = kMaxPositions / c.block_size;
+  a.table_width = (int32_t)(c.table_width < columns ? c.table_width : columns);
   a.requests = (int32_t)c.requests;
   a.tokens = (int32_t)c.tokens;
   a.heads = (int32_t)c.heads;

@@ -108,7 +108,8 @@ nvfp4_status nvfp4_kv_block_tables(const int32_t* context_lens, const int32_t* q
  *   key_cache, value_cache, num_slots, cache_ld  as nvfp4_kv_fp8_store wrote them (16-byte aligned,
  *                 cache_ld a multiple of 16, >= kv_heads * head_dim and < 2^31); 1 <= num_slots < 2^31.
  *   key_scale, value_scale  device, one float each (decode direction).
- *   block_table   device, int32 [requests, table_width], row pitch table_ld.
+ *   block_table   device, int32 [requests, table_width], row pitch table_ld.  Columns from
+ *                 (2^31 - 256) / block_size (rounded down) on are not looked at.
  *   query_start, seq_lens   device, int32[requests + 1] (not decreasing) and int32[requests].
  *   scale         finite; softcap >= 0 and finite (0: no cap).
  *   slopes        device, float[heads], or NULL.

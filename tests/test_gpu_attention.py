@@ -469,3 +469,40 @@ def test_one_prompt_among_single_tokens(requests, longest, hint, dtype, head_dim
         if mods:
             p.options["softcap"] = 20.0
         check(p, f"{requests} requests, one of {longest} at {place}, D={head_dim}", max_query_len=hint, max_seq_len=256)
+
+
+@pytest.mark.parametrize("new,hint", [(1, 64), (1, 2 ** 31 - 1), (200, 64), (200, 2 ** 31 - 1)])
+def test_positions_near_31_bits(new, hint):
+    """All table columns name one block of 2^20 slots; the documents begin close below the last position
+    that is looked at, 2047 * 2^20, and the request is longer still."""
+    import torch
+
+    import bit_block_scaled_nvfp4_amd as nv
+
+    log(f"positions near 2^31, new={new} hint={hint}")
+    bs, D, heads = 1 << 20, 64, 2
+    g = torch.Generator().manual_seed(new)
+    end = 2047 * bs
+    tail = 300  # the slots of the positions before `end` are the block's last ones
+    codes = torch.randint(0, 0x78, (2, tail, D), generator=g, dtype=torch.uint8)
+    kc = torch.full((bs, D), 0x7F, dtype=torch.uint8, device=DEV)  # NaN codes elsewhere
+    vc = torch.full((bs, D), 0x7F, dtype=torch.uint8, device=DEV)
+    kc[-tail:], vc[-tail:] = codes[0].to(DEV), codes[1].to(DEV)
+    q = torch.randn(new, heads, D, generator=g).to(torch.bfloat16)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    one = torch.tensor([0.01], device=DEV)
+    first = end - 1 - torch.arange(new) % (tail - 10)
+    out = nv.nvfp4_kv_fp8_attention(
+        q.to(DEV), kc, vc, one, one, torch.zeros(1, 2048, **i32), torch.tensor([0, new], **i32),
+        torch.tensor([2 ** 31 - 1], **i32), block_size=bs, num_kv_heads=1, doc_start=first.to(**i32),
+        max_seq_len=hint)
+    value = codes.view(torch.float8_e4m3fn).double() * torch.tensor([0.01]).double()
+    x = (q.double().reshape(new * heads, D) @ value[0].t().contiguous()) * D ** -0.5
+    hidden = torch.arange(end - tail, end)[None, :] < first.repeat_interleave(heads)[:, None]
+    p = torch.softmax(x.masked_fill(hidden, float("-inf")), dim=1)
+    want = (p @ value[1]).reshape(new, heads, D)
+    mean = (p @ value[1].abs()).reshape(new, heads, D)
+    # bf16 half step of the result and FP16 half step of each weight; the scores' FP32 sums of 64 products
+    # (|x| <= 64 * |q| * 4.5 / 8 < 150, off by at most 64 * 2^-24 * 150 < 2^-10) twice
+    tol = want.abs() * 2 ** -8 + mean * (2 ** -11 + 2 ** -9) + 2 ** -20
+    assert bool(((out.cpu().double() - want).abs() <= tol).all())
