@@ -64,6 +64,19 @@ def _vector(t, n, dtype, device, name):
     return t.data_ptr()
 
 
+def _row_pitch(t, name):
+    """Elements from one row of the 2-D ``t`` to the next.  A dimension of one row has none that counts, and
+    rows that share elements (an expanded row) have none that the library could take."""
+    rows, width = t.shape
+    if rows <= 1:
+        return max(1, width)
+    pitch = t.stride(0)
+    if pitch < width:
+        raise ValueError(f"{name} must have rows of their own (strides {list(t.stride())}, {width} a row): "
+                         "an expanded or overlapping view needs .contiguous()")
+    return max(1, pitch)
+
+
 def _table(t, rows, device, name):
     torch = _base._torch()
     if t.dtype != torch.int32:
@@ -72,7 +85,7 @@ def _table(t, rows, device, name):
         raise ValueError(f"{name} must be [{rows}, width] with contiguous rows, got {list(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must live on {device}, got {t.device}")
-    return max(1, t.shape[1], t.stride(0) if rows > 1 else 0)
+    return _row_pitch(t, name)
 
 
 def _call(device, fn, *args):
@@ -285,7 +298,7 @@ def nvfp4_kv_fp8_tree_attention(q, key_cache, value_cache, key_scale, value_scal
             raise ValueError(f"tree_mask must have 1 to {MAX_TREE_WORDS} contiguous words a row")
         if tree_mask.device != dev:
             raise ValueError(f"tree_mask must live on {dev}, got {tree_mask.device}")
-        return (tree_mask.data_ptr(), words, max(words, tree_mask.stride(0) if T > 1 else 0),
+        return (tree_mask.data_ptr(), words, _row_pitch(tree_mask, "tree_mask"),
                 None if positions is None else _vector(positions, T, torch.int32, dev, "positions"))
 
     return _attention("nvfp4_kv_fp8_tree_attention", q, key_cache, value_cache, key_scale, value_scale,
