@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 
 import bit_block_scaled_nvfp4_amd as _base
 
@@ -108,6 +109,23 @@ def _cuda(t, name):
     return t.device
 
 
+def _refuse_overlaps(results, inputs, table):
+    """Raise ValueError where a result or the table shares memory with another result or with an input.
+
+    ``results``, ``inputs``: ``(name, address, bytes)``, address 0 without memory; ``table``: address, rows,
+    bytes of a row and bytes from one row to the next (what lies between its rows is not its own)."""
+    at, rows, width, pitch = table
+    for i, (name, p, size) in enumerate(results):
+        for other, q, n in (*results[:i], *inputs):
+            if p and q and size and n and p < q + n and q < p + size:
+                raise ValueError(f"{name} must not share memory with {other}")
+    for name, p, size in (*results, *inputs):
+        if p and at and size and rows * width and p < at + (rows - 1) * pitch + width and at < p + size:
+            row, offset = divmod(max(p - at, 0), pitch)
+            if offset < width or (row + 1 < rows and p + size > at + (row + 1) * pitch):
+                raise ValueError(f"block_table must not share memory with {name}")
+
+
 def nvfp4_kv_block_tables(context_lens, query_lens, free_blocks, block_table, block_size,
                           max_tokens=None, free_start=None, slot_mapping=None, positions=None,
                           query_start=None, seq_lens=None, blocks_needed=None):
@@ -118,7 +136,8 @@ def nvfp4_kv_block_tables(context_lens, query_lens, free_blocks, block_table, bl
     ``free_start`` (1-element int32; None: 0), and entered in ``block_table`` (int32 ``[requests,
     width]``, in place).  Returns ``(slot_mapping int64[max_tokens], positions int32[max_tokens],
     query_start int32[requests + 1], seq_lens int32[requests], blocks_needed int32[1])``; each may be
-    given to be written in place.  Tokens without a block, and padding up to ``max_tokens``, have slot
+    given to be written in place, but shares no memory with another one, with ``block_table`` or with an
+    input (``seq_lens`` of this step can be ``context_lens`` of the next, in a buffer of its own).  Tokens without a block, and padding up to ``max_tokens``, have slot
     -1, which :func:`nvfp4_kv_fp8_store` skips.  ``blocks_needed`` above the free blocks says that
     they did not suffice."""
     torch = _base._torch()
@@ -156,12 +175,26 @@ def nvfp4_kv_block_tables(context_lens, query_lens, free_blocks, block_table, bl
         seq_lens = torch.empty(R, dtype=i32, device=dev)
     if blocks_needed is None:
         blocks_needed = torch.empty(1, dtype=i32, device=dev)
-    _call(dev, lib.nvfp4_kv_block_tables, c, n, R, block_size, f, F, fs, block_table.data_ptr(),
-          block_table.shape[1], ld, _vector(slot_mapping, max_tokens, i64, dev, "slot_mapping"),
-          _vector(positions, max_tokens, i32, dev, "positions"), max_tokens,
-          _vector(query_start, R + 1, i32, dev, "query_start"),
-          _vector(seq_lens, R, i32, dev, "seq_lens"),
-          _vector(blocks_needed, 1, i32, dev, "blocks_needed"))
+    table, W = block_table.data_ptr(), block_table.shape[1]
+    sm = _vector(slot_mapping, max_tokens, i64, dev, "slot_mapping")
+    ps = _vector(positions, max_tokens, i32, dev, "positions")
+    qs = _vector(query_start, R + 1, i32, dev, "query_start")
+    sl = _vector(seq_lens, R, i32, dev, "seq_lens")
+    bn = _vector(blocks_needed, 1, i32, dev, "blocks_needed")
+    # Workgroups read the lengths while others write results.  Ranges are disjoint if and only if, both in
+    # rising order, each ends before the next begins; inputs that share memory, and what lies between a
+    # table's rows, are sorted out afterwards.
+    fs0, span = fs or 0, 4 * ((R - 1) * ld + W) if R * W else 0
+    starts = sorted((c, n, f, fs0, table, sm, ps, qs, sl, bn))
+    ends = sorted((c + 4 * R, n + 4 * R, f + 4 * F, fs0 + 4 if fs0 else 0, table + span, sm + 8 * max_tokens,
+                   ps + 4 * max_tokens, qs + 4 * R + 4, sl + 4 * R, bn + 4))
+    if any(map(operator.gt, ends, starts[1:])):
+        _refuse_overlaps((("slot_mapping", sm, 8 * max_tokens), ("positions", ps, 4 * max_tokens),
+                          ("query_start", qs, 4 * R + 4), ("seq_lens", sl, 4 * R), ("blocks_needed", bn, 4)),
+                         (("context_lens", c, 4 * R), ("query_lens", n, 4 * R), ("free_blocks", f, 4 * F),
+                          ("free_start", fs0, 4 if fs0 else 0)), (table, R, 4 * W, 4 * ld))
+    _call(dev, lib.nvfp4_kv_block_tables, c, n, R, block_size, f, F, fs, table, W, ld, sm, ps, max_tokens, qs,
+          sl, bn)
     return slot_mapping, positions, query_start, seq_lens, blocks_needed
 
 
