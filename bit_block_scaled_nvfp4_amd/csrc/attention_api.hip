@@ -149,7 +149,9 @@ nvfp4_status run(const Call& c, const int32_t* doc_start, const int32_t* prefix_
   a.bs = nvfp4::make_fast_div((uint32_t)c.block_size);
   a.group = nvfp4::make_fast_div((uint32_t)group);
   a.scale = c.scale;
-  a.cap = c.softcap;
+  // below 1e-9 the capped scores change no weight in FP32, and 1e37 bounds the scores that count: between them
+  // the cap's factors are finite
+  a.cap = c.softcap > 0.0f ? (c.softcap < 1e-9f ? 1e-9f : (c.softcap > 1e37f ? 1e37f : c.softcap)) : 0.0f;
   if (p.workers) {
     const int64_t rows = 2 * (int64_t)p.workers * p.rows;
     a.part = static_cast<float*>(c.workspace);

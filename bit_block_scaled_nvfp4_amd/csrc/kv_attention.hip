@@ -135,7 +135,7 @@ struct State {
   int32_t lo_all, hi_all;  // positions every row of the tile sees: [lo_all, hi_all)
 };
 
-template <int D, bool BF16, int NQ, bool MODS>
+template <int D, bool BF16, int NQ, Scores SCORES>
 __device__ __forceinline__ void step(const Segment& sg, const Request& rq, const Keys<D>& kc, Values<D>& vc, int32_t slot,
                                      int32_t j0, float c, float cap, int lane, State<D, NQ>& s) {
   const int g = lane >> 4;
@@ -165,17 +165,25 @@ __device__ __forceinline__ void step(const Segment& sg, const Request& rq, const
   const bool whole = in_cache == ~0ull && j0 >= s.lo_all && j0 + kStep <= s.hi_all;
   // scores are x cm + base, in units of log2
   float cm = c, base = 0.0f;
-  if constexpr (MODS) {
+  if constexpr (SCORES != Scores::Plain) {
     if (cap > 0.0f) {
-      const float to_r = cm / cap * 2.0f;
+      if constexpr (SCORES == Scores::WideCap) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int n = 0; n < NQ; ++n)
+          for (int n = 0; n < NQ; ++n) cap_wide<4>(x[t][n], c, cap);
+        cm = 1.0f;
+      } else {
+        const float to_r = cm / cap * 2.0f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[t][n][i] = cap_term(x[t][n][i], to_r);
-      base = cap * kLog2e;
-      cm = -2.0f * base;
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[t][n][i] = cap_term(x[t][n][i], to_r);
+        base = cap * kLog2e;
+        cm = -2.0f * base;
+      }
     }
   }
 #pragma unroll
@@ -184,7 +192,7 @@ __device__ __forceinline__ void step(const Segment& sg, const Request& rq, const
     for (int n = 0; n < NQ; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[t][n][i] = __builtin_fmaf(x[t][n][i], cm, base);
-  if constexpr (MODS) {
+  if constexpr (SCORES != Scores::Plain) {
     const AttnArgs& a = args();
     if (a.slopes) {
       const int32_t* positions = a.tree ? a.positions : nullptr;
@@ -308,7 +316,7 @@ __device__ __forceinline__ void step(const Segment& sg, const Request& rq, const
   }
 }
 
-template <int D, bool BF16, int NQ, bool MODS>
+template <int D, bool BF16, int NQ, Scores SCORES>
 __device__ __forceinline__ void segment(const Segment& sg, bool split, int32_t worker, float* lds) {
   const AttnArgs& a = args();
   constexpr int kRows = 16 * NQ;
@@ -317,7 +325,7 @@ __device__ __forceinline__ void segment(const Segment& sg, bool split, int32_t w
   const int g = lane >> 4, d16 = lane & 15;
   const Request rq = request_of(a, sg.r);
   State<D, NQ> s;
-  const float c = a.scale * *a.ks * kLog2e, cap = MODS ? a.cap : 0.0f;
+  const float c = a.scale * *a.ks * kLog2e, cap = SCORES != Scores::Plain ? a.cap : 0.0f;
 
   int32_t lo_min = 0x7FFFFFFF, hi_max = 0, lo_max = 0, hi_min = 0x7FFFFFFF;
 #pragma unroll
@@ -392,14 +400,14 @@ __device__ __forceinline__ void segment(const Segment& sg, bool split, int32_t w
       __builtin_amdgcn_sched_barrier(0);
       load_values<D, NQ == 1>(a, s0, vbase, ln, v);
       if (u > u0) load_keys<D, NQ == 1>(a, s1, kbase, ln, k1);
-      step<D, BF16, NQ, MODS>(sg, rq, k0, v, s0, u * kUnit + wave * kStep, c, cap, ln, s);
+      step<D, BF16, NQ, SCORES>(sg, rq, k0, v, s0, u * kUnit + wave * kStep, c, cap, ln, s);
       if (u - 1 < u0) break;
       s0 = slots(e2, u - 2);
       e1 = entries(u - 3);
       __builtin_amdgcn_sched_barrier(0);
       load_values<D, NQ == 1>(a, s1, vbase, ln, v);
       if (u - 1 > u0) load_keys<D, NQ == 1>(a, s0, kbase, ln, k0);
-      step<D, BF16, NQ, MODS>(sg, rq, k1, v, s1, (u - 1) * kUnit + wave * kStep, c, cap, ln, s);
+      step<D, BF16, NQ, SCORES>(sg, rq, k1, v, s1, (u - 1) * kUnit + wave * kStep, c, cap, ln, s);
       if (u - 2 < u0) break;
     }
   }
@@ -472,7 +480,7 @@ __device__ __forceinline__ void segment(const Segment& sg, bool split, int32_t w
   __syncthreads();  // the next segment writes ml and the tiles again
 }
 
-template <int D, bool BF16, int NQ, bool MODS>
+template <int D, bool BF16, int NQ, Scores SCORES>
 __global__ void __launch_bounds__(kThreads, stream_groups(D, 16 * NQ)) attention_stream_kernel(AttnArgs) {
   constexpr int kRows = 16 * NQ;
   __shared__ __align__(16) float lds[kWaves * 16 * (D + 4) + kWaves * kRows * 2];
@@ -488,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, stream_groups(D, 16 * NQ)) attention
     s.u0 = 0;
     s.u1 = (int32_t)(((uint32_t)q.keys + kUnit - 1) / kUnit);
     const int32_t tiles = (int32_t)(((uint32_t)q.count * a.group.d + kRows - 1) / kRows);
-    for (s.tile = blockIdx.z; s.tile < tiles; s.tile += gridDim.z) segment<D, BF16, NQ, MODS>(s, false, 0, lds);
+    for (s.tile = blockIdx.z; s.tile < tiles; s.tile += gridDim.z) segment<D, BF16, NQ, SCORES>(s, false, 0, lds);
     return;
   }
   share.begin(kRows, kUnit);
@@ -496,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, stream_groups(D, 16 * NQ)) attention
   if (threadIdx.x == 0) header->last_worker = -1;
   while (share.next(kRows, kUnit, s)) {
     if (s.first && !s.last && threadIdx.x == 0) *header = Header{s.r, s.tile, s.kv_head, s.last_worker, share.worker, {0, 0, 0}};
-    segment<D, BF16, NQ, MODS>(s, true, uniform(share.worker), lds);
+    segment<D, BF16, NQ, SCORES>(s, true, uniform(share.worker), lds);
   }
 }
 
@@ -593,18 +601,19 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(AttnArgs a, in
   }
 }
 
-template <int D, bool BF16, int NQ, bool MODS>
+template <int D, bool BF16, int NQ, Scores SCORES>
 void launch_stream(const AttnArgs& a, hipStream_t stream) {
   const dim3 grid = a.workers ? dim3((uint32_t)a.workers) : dim3((uint32_t)a.kv_heads, (uint32_t)a.requests, (uint32_t)a.row_tiles);
-  hipLaunchKernelGGL((attention_stream_kernel<D, BF16, NQ, MODS>), grid, dim3(kThreads), 0, stream, a);
+  hipLaunchKernelGGL((attention_stream_kernel<D, BF16, NQ, SCORES>), grid, dim3(kThreads), 0, stream, a);
 }
 
 template <int D, bool BF16, int NQ>
 void launch_stream(const AttnArgs& a, hipStream_t stream) {
-  if (a.cap > 0.0f || a.slopes)
-    launch_stream<D, BF16, NQ, true>(a, stream);
-  else
-    launch_stream<D, BF16, NQ, false>(a, stream);
+  switch (scores_of(a)) {
+    case Scores::Plain: launch_stream<D, BF16, NQ, Scores::Plain>(a, stream); break;
+    case Scores::Modified: launch_stream<D, BF16, NQ, Scores::Modified>(a, stream); break;
+    case Scores::WideCap: launch_stream<D, BF16, NQ, Scores::WideCap>(a, stream); break;
+  }
 }
 
 template <int D, bool BF16>

@@ -174,9 +174,63 @@ __device__ __forceinline__ int32_t key_position(const int32_t* positions, const 
 // The cap in units of log2(e): cap tanh(y) log2(e) = L - 2 L r with L = cap log2(e) and
 // r = 1 / (exp(2 y) + 1).  This is r, for to_r = 2 log2(e) / cap times what turns x into a score; the
 // product with -2 L joins the scaling that every score goes through.  r is off by a few 2^-24, the
-// capped score by as much times 2 L.
+// capped score by as much times 2 L: an error that goes with the cap, not with the score, so it is used
+// up to kSmallCap only (there it is 3e-5, a fifteenth of the rounding of the exponentials to FP16).
 __device__ __forceinline__ float cap_term(float x, float to_r) {
   return __builtin_amdgcn_rcpf(exp2_of(x * to_r) + 1.0f);
+}
+
+constexpr float kSmallCap = 128.0f;
+
+// Where the cap is larger: y = x / cap (x a score) and the capped score in units of log2(e).  For
+// |y| >= 1/2 the error above is one of the score itself.  Below, tanh(y) / y is Lambert's continued
+// fraction 1 / (1 + y^2 / (3 + y^2 / (5 + y^2 / 7))) = (105 + 10 y^2) / (105 + 45 y^2 + y^4), off by less
+// than 2^-24 of itself there.
+__device__ __forceinline__ float capped_near(float x, float c, float to_y) {
+  const float y = x * to_y, z = y * y;
+  return (x * c) * (__builtin_fmaf(z, 10.0f, 105.0f) * __builtin_amdgcn_rcpf(__builtin_fmaf(z, z + 45.0f, 105.0f)));
+}
+
+__device__ __forceinline__ float capped_wide(float x, float c, float to_y, float to_r, float base) {
+  const float far = __builtin_fmaf(cap_term(x, to_r), -2.0f * base, base);
+  return __builtin_fabsf(x * to_y) < 0.5f ? capped_near(x, c, to_y) : far;
+}
+
+// N scores of a lane.  Scores rarely reach half of a wide cap: the other form is formed where one of the
+// wavefront's does (8192-token prompt, 32 heads of 128 dims, cap 200: 911 us, both forms of every score
+// 1086 us, the form for small caps 728 us).
+template <int N, typename V>
+__device__ __forceinline__ void cap_wide(V& x, float c, float cap) {
+  float to_y = c / (cap * kLog2e), top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) top = __builtin_fmaxf(top, __builtin_fabsf(x[i]));
+  if (rarely(__any(!(top * __builtin_fabsf(to_y) < 0.5f)))) {
+    asm volatile("" : "+v"(to_y));  // the two sides share nothing: it would be kept through the branch
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      x[i] = capped_wide(x[i], c, to_y, 2.0f * kLog2e * to_y, cap * kLog2e);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      x[i] = capped_near(x[i], c, to_y);
+      if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
+
+// What becomes of a score before the softmax.  A kernel for each: what one of them needs costs the others
+// registers (the wide cap beside the other, behind a branch: up to 27 more spilled in the tiled kernel).
+enum class Scores {
+  Plain,
+  Modified,  // capped by kSmallCap at most, or biased, or both
+  WideCap    // capped by more, and biased where slopes is given
+};
+
+inline Scores scores_of(const AttnArgs& a) {
+  if (a.cap > kSmallCap) return Scores::WideCap;
+  return a.cap > 0.0f || a.slopes ? Scores::Modified : Scores::Plain;
 }
 
 // ---- cache rows -----------------------------------------------------------------------------

@@ -181,14 +181,14 @@ __device__ __forceinline__ bool stage(const Fetched& f, const There<D>& there, b
 }
 
 // Score of element i of x[n], less m: x cm + (slope * offset + (bias - m)).
-template <bool MODS>
+template <Scores SCORES>
 __device__ __forceinline__ float score(float x, float cm, float slope, float shift, int n, int i) {
-  if constexpr (MODS) shift = __builtin_fmaf(slope, (float)(32 * n + 8 * (i >> 2) + (i & 3)), shift);
+  if constexpr (SCORES != Scores::Plain) shift = __builtin_fmaf(slope, (float)(32 * n + 8 * (i >> 2) + (i & 3)), shift);
   return __builtin_fmaf(x, cm, shift);
 }
 
 // exp2 of the scores less m in FP16, in the output product's operand layout; returns their sum in FP32.
-template <int N, bool MODS>
+template <int N, Scores SCORES>
 __device__ __forceinline__ float exponentials(const f32x16 (&x)[N], float cm, float slope, float shift, u32x4 (&p)[2 * N]) {
   float sum = 0.0f;
 #pragma unroll
@@ -197,7 +197,7 @@ __device__ __forceinline__ float exponentials(const f32x16 (&x)[N], float cm, fl
     for (int u = 0; u < 2; ++u) {
       float e[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = exp2_of(score<MODS>(x[n][8 * u + i], cm, slope, shift, n, 8 * u + i));
+      for (int i = 0; i < 8; ++i) e[i] = exp2_of(score<SCORES>(x[n][8 * u + i], cm, slope, shift, n, 8 * u + i));
       sum += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
       p[2 * n + u] = u32x4{pack_f16(e[0], e[1]), pack_f16(e[2], e[3]), pack_f16(e[4], e[5]), pack_f16(e[6], e[7])};
     }
@@ -221,7 +221,7 @@ struct WaveState {
   int32_t lo_min, hi_max, lo_all, hi_all;  // over the wavefront's rows
 };
 
-template <int D, bool BF16, bool MODS>
+template <int D, bool BF16, Scores SCORES>
 __device__ __forceinline__ void multiply(float cap, const Request& rq, const char* qt, const char* kt, const char* vt, const There<D>& there,
                                          bool nans, bool moved, float* away, const Segment& now, uint32_t my_row, int32_t j0, float c, float inv_cap, int lane, WaveState<D>& s) {
   constexpr int N = kKeys<D> / 32;
@@ -243,19 +243,25 @@ __device__ __forceinline__ void multiply(float cap, const Request& rq, const cha
   // element adds its offset in the tile
   float cm = c, bias = 0.0f;
   uint32_t none = kMinusInf;  // times cm: -inf
-  if constexpr (MODS) {
+  if constexpr (SCORES != Scores::Plain) {
     float base = 0.0f;
     if (cap > 0.0f) {
-      const float to_r = c * inv_cap * 2.0f;
+      if constexpr (SCORES == Scores::WideCap) {
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
+        for (int n = 0; n < N; ++n) cap_wide<16>(x[n], c, cap);
+        cm = 1.0f;
+      } else {
+        const float to_r = c * inv_cap * 2.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[n][i] = cap_term(x[n][i], to_r);
-        __builtin_amdgcn_sched_barrier(0);
+        for (int n = 0; n < N; ++n) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[n][i] = cap_term(x[n][i], to_r);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        base = cap * kLog2e;
+        cm = -2.0f * base;
+        none = kPlusInf;
       }
-      base = cap * kLog2e;
-      cm = -2.0f * base;
-      none = kPlusInf;
     }
     bias = __builtin_fmaf(s.slope, (float)(j0 + 4 * h - s.pos), base);
     if (rarely(moved && j0 + kKeys<D> > rq.ctx)) {
@@ -295,20 +301,20 @@ __device__ __forceinline__ void multiply(float cap, const Request& rq, const cha
     }
   }
   u32x4 p[2 * N];
-  float sum = exponentials<N, MODS>(x, cm, s.slope, bias - s.m, p);
+  float sum = exponentials<N, SCORES>(x, cm, s.slope, bias - s.m, p);
   if (rarely(__any(sum > kRaise))) {
-    float top = score<MODS>(x[0][0], cm, s.slope, bias, 0, 0);
+    float top = score<SCORES>(x[0][0], cm, s.slope, bias, 0, 0);
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, score<MODS>(x[n][i], cm, s.slope, bias, n, i));
+      for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, score<SCORES>(x[n][i], cm, s.slope, bias, n, i));
     const float m = __builtin_fmaxf(s.m, other_half_max(top));
     const float f = exp2_of(s.m - m);
     s.m = m;
     s.l *= f;
 #pragma unroll
     for (int d = 0; d < D / 32; ++d) s.acc[d] *= f;
-    sum = exponentials<N, MODS>(x, cm, s.slope, bias - m, p);
+    sum = exponentials<N, SCORES>(x, cm, s.slope, bias - m, p);
   }
   s.l += sum;
   __builtin_amdgcn_sched_barrier(0);
@@ -355,7 +361,7 @@ struct Shared {
   Share<kThreads> share;
 };
 
-template <int D, bool BF16, bool MODS, bool SPLIT>
+template <int D, bool BF16, Scores SCORES, bool SPLIT>
 __device__ __forceinline__ void segment(const Segment& sg, Shared<D>& lds) {
   const AttnArgs& a = args();
   constexpr int BN = kKeys<D>;
@@ -372,7 +378,7 @@ __device__ __forceinline__ void segment(const Segment& sg, Shared<D>& lds) {
   const uint32_t keep = c == 0.0f ? 0u : 0xFFFFFFFFu;
   if (c == 0.0f) c = 1.0f;
   const float inv_cap = a.cap > 0.0f ? 1.0f / a.cap : 0.0f;
-  const bool moved = MODS && a.tree && a.slopes && a.positions;
+  const bool moved = SCORES != Scores::Plain && a.tree && a.slopes && a.positions;
   const uint32_t my_row = (uint32_t)(sg.tile * kRows + 32 * wave + r);
   const Row row = row_of(a, sg.r, rq, sg.kv_head, my_row);
   s.lo = row.lo;
@@ -510,7 +516,7 @@ __device__ __forceinline__ void segment(const Segment& sg, Shared<D>& lds) {
 #pragma unroll
           for (int w = 0; w < kWaves; ++w) nans |= lds.nans[b][w];
         }
-        multiply<D, BF16, MODS>(a.cap, rq, qt, lds.tiles[b][0], lds.tiles[b][1], cur, uniform(nans) != 0, moved, lds.away[wave], lds.share.segment, my_row, j0, c, inv_cap, lane, s);
+        multiply<D, BF16, SCORES>(a.cap, rq, qt, lds.tiles[b][0], lds.tiles[b][1], cur, uniform(nans) != 0, moved, lds.away[wave], lds.share.segment, my_row, j0, c, inv_cap, lane, s);
       }
       cur = nxt;
       nxt = nx2;
@@ -560,8 +566,7 @@ __device__ __forceinline__ void segment(const Segment& sg, Shared<D>& lds) {
 // segment() costs the others registers.
 enum class Work { Place, Search, Share };
 
-// MODS: scores are capped or biased.
-template <int D, bool BF16, bool MODS, Work WORK>
+template <int D, bool BF16, Scores SCORES, Work WORK>
 __global__ void __launch_bounds__(kThreads) attention_tiled_kernel(AttnArgs) {
   __shared__ __align__(16) Shared<D> lds;
   Segment s;
@@ -579,43 +584,47 @@ __global__ void __launch_bounds__(kThreads) attention_tiled_kernel(AttnArgs) {
     for (int32_t k = blockIdx.z; k < tiles; k += gridDim.z) {
       s.tile = tiles - 1 - k;
       if (threadIdx.x == 0) lds.share.segment = s;  // read again behind segment()'s first barrier
-      segment<D, BF16, MODS, false>(s, lds);
+      segment<D, BF16, SCORES, false>(s, lds);
     }
   } else if constexpr (WORK == Work::Search) {
     if (threadIdx.x == 0) lds.share.worker = blockIdx.y;
     __syncthreads();
-    while (lds.share.next_tile(kRows, kKeys<D>, s)) segment<D, BF16, MODS, false>(s, lds);
+    while (lds.share.next_tile(kRows, kKeys<D>, s)) segment<D, BF16, SCORES, false>(s, lds);
   } else {
     lds.share.begin(kRows, kKeys<D>);
     Header* header = reinterpret_cast<Header*>(args().headers) + blockIdx.x;
     if (threadIdx.x == 0) header->last_worker = -1;
     while (lds.share.next(kRows, kKeys<D>, s)) {
       if (s.first && !s.last && threadIdx.x == 0) *header = Header{s.r, s.tile, s.kv_head, s.last_worker, lds.share.worker, {0, 0, 0}};
-      segment<D, BF16, MODS, true>(s, lds);
+      segment<D, BF16, SCORES, true>(s, lds);
     }
   }
 }
 
-template <int D, bool BF16, bool MODS>
+template <int D, bool BF16, Scores SCORES>
 void launch(const AttnArgs& a, hipStream_t stream) {
   const dim3 threads(kThreads), workers((uint32_t)a.workers), search((uint32_t)a.kv_heads, (uint32_t)a.all_tiles);
   const dim3 place((uint32_t)a.kv_heads, (uint32_t)a.requests, (uint32_t)a.row_tiles);
   if (a.workers)
-    hipLaunchKernelGGL((attention_tiled_kernel<D, BF16, MODS, Work::Share>), workers, threads, 0, stream, a);
+    hipLaunchKernelGGL((attention_tiled_kernel<D, BF16, SCORES, Work::Share>), workers, threads, 0, stream, a);
   else if (a.all_tiles)
-    hipLaunchKernelGGL((attention_tiled_kernel<D, BF16, MODS, Work::Search>), search, threads, 0, stream, a);
+    hipLaunchKernelGGL((attention_tiled_kernel<D, BF16, SCORES, Work::Search>), search, threads, 0, stream, a);
   else
-    hipLaunchKernelGGL((attention_tiled_kernel<D, BF16, MODS, Work::Place>), place, threads, 0, stream, a);
+    hipLaunchKernelGGL((attention_tiled_kernel<D, BF16, SCORES, Work::Place>), place, threads, 0, stream, a);
+}
+
+template <int D, bool BF16>
+void launch(const AttnArgs& a, hipStream_t stream) {
+  switch (scores_of(a)) {
+    case Scores::Plain: launch<D, BF16, Scores::Plain>(a, stream); break;
+    case Scores::Modified: launch<D, BF16, Scores::Modified>(a, stream); break;
+    case Scores::WideCap: launch<D, BF16, Scores::WideCap>(a, stream); break;
+  }
 }
 
 template <int D>
 void launch(const AttnArgs& a, bool bf16, hipStream_t stream) {
-  const bool mods = a.cap > 0.0f || a.slopes;
-  if (bf16) {
-    if (mods) launch<D, true, true>(a, stream); else launch<D, true, false>(a, stream);
-  } else {
-    if (mods) launch<D, false, true>(a, stream); else launch<D, false, false>(a, stream);
-  }
+  if (bf16) launch<D, true>(a, stream); else launch<D, false>(a, stream);
 }
 
 }  // namespace

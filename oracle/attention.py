@@ -84,7 +84,7 @@ def attention(q, key_cache, value_cache, key_scale, value_scale, block_table, qu
                                                    below the fraction
       + 2 A (N + 64) 2^-23                         sums over N keys, in any order, and their joining
 
-    dx = 2^-23 ((head_dim + 8) max_j scale sum|q k| + 8 cap + 4 |bias|max + 8)."""
+    dx = 2^-23 ((head_dim + 8) X + 8 min(cap, max(128, X)) + 4 |bias|max + 8),  X = max_j scale sum|q k|."""
     q = np.asarray(q, np.float64)
     T, H, D = q.shape
     G = H // kv_heads
@@ -142,7 +142,7 @@ def attention(q, key_cache, value_cache, key_scale, value_scale, block_table, qu
                 total = w.sum()
                 o[t, h] = (w @ v) / total
                 A = (w @ np.abs(v)) / total
-                dx = 2.0 ** -23 * ((D + 8) * mag + 8 * softcap + 4 * big + 8)
+                dx = 2.0 ** -23 * ((D + 8) * mag + 8 * min(softcap, max(128.0, mag)) + 4 * big + 8)
                 tol[t, h] = (out_eps / 2 * np.abs(o[t, h]) + A * (2.0 ** -11 + 2 * dx + 2 * (len(w) + 64) * 2.0 ** -23)
                              + 2.0 ** -25 * np.abs(v).sum(0) / total)
     return o, tol

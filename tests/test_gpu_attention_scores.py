@@ -1,0 +1,79 @@
+"""GPU parity of what becomes of a score in the attentions over the paged FP8 cache, at the ends of its range, against
+the binary64 oracle under its derived tolerance: caps from the smallest number to the largest."""
+
+import numpy as np
+import pytest
+
+from .attention_util import Problem, compare, tree_mask
+from .gpu_util import log
+
+pytestmark = pytest.mark.gpu
+
+#: new tokens of 4 heads a KV head: tiles of 16, 32 and 256 rows
+NEW = [1, 9, 40]
+
+
+def check(p, what, **kw):
+    log(f"attention scores {what}")
+    want, tol = p.oracle()
+    got = p.run(**kw)
+    compare(got, want, tol, what)
+    return got
+
+
+def problem(new, head_dim, dtype="bf16", seed=0, tree=False, slopes=False, positions=False, q_std=2.0):
+    lens = [(700, new), (33, max(1, new // 2)), (0, new), (300, new)]
+    p = Problem(lens, 8, 2, head_dim, dtype=dtype, seed=100 + new + seed, q_std=q_std)
+    counts = [n for _, n in lens]
+    if tree:
+        p.options["tree_mask"] = tree_mask(p.rng, counts)
+    if slopes:
+        p.options["slopes"] = np.linspace(0.01, 0.7, 8).astype(np.float32)
+    if positions:
+        p.options["positions"] = np.concatenate([c + p.rng.integers(0, 4, n) for c, n in lens])
+    return p
+
+
+def hints(new, split):
+    """Bounds under which the longest sequence is shared among workgroups and joined, or not."""
+    return dict(max_query_len=new, max_seq_len=100000 if split else (1000 if new < 40 else 100))
+
+
+@pytest.mark.parametrize("cap", [1e-45, 1e-38, 1e-8, 1e-3, 128.0, 129.0, 1e3, 1e5, 1e6, 1e9, 3e38])
+@pytest.mark.parametrize("new", NEW)
+@pytest.mark.parametrize("head_dim", [64, 128, 256])
+def test_caps_of_every_size(cap, new, head_dim):
+    p = problem(new, head_dim)
+    p.q[::7] = 0  # scores of exactly 0
+    p.options["softcap"] = float(np.float32(cap))
+    check(p, f"cap={cap} new={new} D={head_dim}", **hints(new, False))
+
+
+@pytest.mark.parametrize("cap", [129.0, 250.0])
+@pytest.mark.parametrize("new", NEW)
+def test_scores_that_reach_a_wide_cap(cap, new):
+    p = problem(new, 64, dtype="f16")
+    p.scale = 4.0  # scores of about +- 100
+    p.options["softcap"] = cap
+    check(p, f"reached cap={cap} new={new}", **hints(new, False))
+
+
+@pytest.mark.parametrize("split", [False, True])
+@pytest.mark.parametrize("new", NEW)
+@pytest.mark.parametrize("head_dim", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_every_kernel_with_a_wide_cap(dtype, head_dim, new, split):
+    for tree, slopes in ((False, False), (False, True), (True, True)):
+        p = problem(new, head_dim, dtype, seed=7, tree=tree, slopes=slopes, positions=tree)
+        p.options["softcap"] = 1e5
+        check(p, f"wide cap {dtype} D={head_dim} new={new} split={split} tree={tree}", **hints(new, split))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("head_dim", [64, 128, 256])
+def test_a_wide_cap_where_row_tiles_are_searched(dtype, head_dim):
+    lens = [((i * 7) % 40, i % 3 % 2) for i in range(60)]
+    lens[20] = (11, 300)
+    p = Problem(lens, 4, 2, head_dim, dtype=dtype, seed=3, pad_tokens=3)
+    p.options["softcap"] = 1e5
+    check(p, f"wide cap searched {dtype} D={head_dim}", max_query_len=300, max_seq_len=256)
