@@ -294,8 +294,11 @@ def nvfp4_kv_fp8_attention(q, key_cache, value_cache, key_scale, value_scale, bl
     positions of its ``seq_lens[r]``, whose rows the cache already holds; ``block_table`` says where.
     Causal; ``softcap`` > 0 caps scores by ``softcap * tanh(x / softcap)``, ``slopes`` (float32
     ``[heads]``) adds ``slope * (key position - query position)``, ``doc_start`` (int32 ``[tokens]``)
-    hides the positions before each token's document, ``prefix_lens`` (int32 ``[requests]``) shows each
-    request's prefix to all its tokens.  Rows that see nothing are zero; rows of no request are left as
+    hides the positions before each token's document, ``prefix_lens`` (int32 ``[requests]``) shows the
+    positions below it ahead of the causal order too: by itself, each request's prefix to all its tokens;
+    with ``doc_start``, what of it does not lie before the token's document, so that the two belong together
+    where the prefix ends within the first document (one that reaches further shows a document's tokens the
+    beginning of the next one, and none is shared by all documents).  Rows that see nothing are zero; rows of no request are left as
     they were.  ``max_query_len`` and ``max_seq_len`` (bounds of the requests' lengths) only choose how
     the work is divided.  Single tokens in a call with prompts cost as much as 256 rows each over their
     context: many of them over long contexts are faster in a call of their own.  Returns ``out`` in q's

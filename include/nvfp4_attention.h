@@ -88,9 +88,16 @@ nvfp4_status nvfp4_kv_block_tables(const int32_t* context_lens, const int32_t* q
  *   x_j = x_j + slopes[h] * (j - p_t)                    where slopes is given
  *   out = sum_j exp(x_j) V_j / sum_j exp(x_j)            over the visible j
  * j is visible when doc_start[t] <= j (document mask: the position at which the token's document
- * begins; 0 where doc_start is NULL) and j <= p_t or j < prefix_lens[r] (prefix mask: a prefix that
- * every token of the request sees; 0 where prefix_lens is NULL).  A position whose table column or
- * slot lies outside the table or the cache is not visible.  A row that sees nothing gives zeros.
+ * begins; 0 where doc_start is NULL) and, besides, j <= p_t or j < prefix_lens[r] (prefix mask: the
+ * positions below the prefix's end are seen ahead of the causal order too; 0 where prefix_lens is NULL).
+ * By itself the prefix mask shows the prefix to every token of the request.  Together with documents it
+ * is bounded by them: a token sees of the prefix what lies in or behind the beginning of its own document.
+ * So the two belong together where the prefix ends within the request's first document; then only that
+ * document's tokens see it, all of it, and no document sees another.  A prefix that ends further on shows
+ * a document's tokens what follows their document up to there (the masks say where a token's document
+ * begins, not where it ends).  A prefix that all documents share is not among these masks.
+ * A position whose table column or slot lies outside the table or the cache is not visible.  A row that
+ * sees nothing gives zeros.
  * Rows t < query_start[0] or >= query_start[requests], and rows of other requests' gaps, are left as
  * they were.  Values in positions a row does not see have no effect on it, NaN codes included.
  *

@@ -12,7 +12,8 @@ T1  request r with c cached and n new tokens holds ceil(c / bs) blocks and needs
 A1  query row i of the n of a request stands at position p = len - n + i; x_j = scale * q . K_j,
     then cap * tanh(x / cap), then + slope * (pos_j - p); out = sum exp(x_j) V_j / sum exp(x_j) over
     the visible j, zeros when none is.
-A2  prompts: doc_start <= j and (j <= p or j < prefix).  Trees: j < len - n, or bit j - (len - n) set.
+A2  prompts: doc_start <= j and (j <= p or j < prefix), so documents bound the prefix.
+    Trees: j < len - n, or bit j - (len - n) set.
 A3  positions whose table column, block or slot is outside the table or the cache are not visible.
 """
 
