@@ -233,7 +233,7 @@ __device__ __forceinline__ void step(const Segment& sg, const Request& rq, const
       float top = x[0][n][0];
 #pragma unroll
       for (int i = 1; i < 8; ++i) top = __builtin_fmaxf(top, x[i >> 2][n][i & 3]);
-      const float m = __builtin_fmaxf(s.m[n], max_over_groups(top));
+      const float m = __builtin_fmaxf(s.m[n], max_over_groups(top) - kBelow);
       const float f = exp2_of(s.m[n] - m);
       s.m[n] = m;
       s.l[n] *= f;

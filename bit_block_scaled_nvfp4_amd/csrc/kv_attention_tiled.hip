@@ -303,11 +303,12 @@ __device__ __forceinline__ void multiply(float cap, const Request& rq, const cha
   u32x4 p[2 * N];
   float sum = exponentials<N, SCORES>(x, cm, s.slope, bias - s.m, p);
   if (rarely(__any(sum > kRaise))) {
-    float top = score<SCORES>(x[0][0], cm, s.slope, bias, 0, 0);
+    const float lower = bias - kBelow;
+    float top = score<SCORES>(x[0][0], cm, s.slope, lower, 0, 0);
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, score<SCORES>(x[n][i], cm, s.slope, bias, n, i));
+      for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, score<SCORES>(x[n][i], cm, s.slope, lower, n, i));
     const float m = __builtin_fmaxf(s.m, other_half_max(top));
     const float f = exp2_of(s.m - m);
     s.m = m;

@@ -103,9 +103,8 @@ nvfp4_status nvfp4_kv_block_tables(const int32_t* context_lens, const int32_t* q
  *
  * Arithmetic: q . K is formed by MFMA with exact FP32 products of the query type and the decoded
  * codes, FP32 sums, FP32 scores and softmax statistics; exp(x - reference) is rounded once to FP16
- * (by at most 2^-11 relative, or 2^-25 absolute below 2^-14) for the product with the decoded values,
- * summed in FP32; the result is rounded once to the query type.  The reference is one of the row's
- * scores.  Scores (times log2(e)) of -1e37 and less count as -infinity.  The cap adds an error of at most
+ * (by at most 2^-11 relative, or 2^-29 of the row's largest where that is more) for the product with the
+ * decoded values, summed in FP32; the result is rounded once to the query type.  Scores (times log2(e)) of -1e37 and less count as -infinity.  The cap adds an error of at most
  * 2^-20 min(softcap, max(128, |x_j|)) to a score; caps below 1e-9 count as 1e-9, above 1e37 as 1e37.
  *
  *   q             device, [tokens, heads, head_dim] of dtype (BF16 or F16), token and head strides in

@@ -74,13 +74,16 @@ def attention(q, key_cache, value_cache, key_scale, value_scale, block_table, qu
     """``(out, tolerance)`` in binary64.  ``tree``: bool ``[tokens, drafted]`` (drafted trees), else
     prompts.  ``out``: initial contents, kept where no request owns a row.  The tolerance of an element
     counts the roundings of an FP32 computation whose exponentials are rounded to FP16 (half steps
-    2^-24 and 2^-11; below 2^-14 an absolute 2^-25) and whose result is rounded with relative step
-    ``out_eps``:
+    2^-24 and 2^-11; below 2^-14 an absolute 2^-25, where a row's largest weight is 2^4 at least) and whose
+    result is rounded with relative step ``out_eps``:
 
-      out_eps / 2 |o|                              the last rounding
-      + A 2^-11 + 2^-25 sum|v| / sum p'            exponentials to FP16; A = sum p |v| / sum p, and
+      out_eps / 2 |o|, 2^-25 at least for FP16     the last rounding (FP16 numbers below 2^-14 lie 2^-24
+                                                   apart: 8.518 2^-24 is rounded to 9 2^-24, off by
+                                                   0.48 steps; BF16's 2^-133 count as nothing)
+      + A 2^-11 + 2^-29 sum|v| / sum p'            exponentials to FP16; A = sum p |v| / sum p, and
                                                    p' = p / max p (the kernel's reference is at most
-                                                   the maximum, so its sum is at least this one)
+                                                   2^-4 of the maximum, so its sum is at least 2^4
+                                                   times this one)
       + 2 A dx                                     scores off by dx: p changes by exp(dx), above and
                                                    below the fraction
       + 2 A (N + 64) 2^-23                         sums over N keys, in any order, and their joining
@@ -144,6 +147,7 @@ def attention(q, key_cache, value_cache, key_scale, value_scale, block_table, qu
                 o[t, h] = (w @ v) / total
                 A = (w @ np.abs(v)) / total
                 dx = 2.0 ** -23 * ((D + 8) * mag + 8 * min(softcap, max(128.0, mag)) + 4 * big + 8)
-                tol[t, h] = (out_eps / 2 * np.abs(o[t, h]) + A * (2.0 ** -11 + 2 * dx + 2 * (len(w) + 64) * 2.0 ** -23)
-                             + 2.0 ** -25 * np.abs(v).sum(0) / total)
+                least = 2.0 ** -25 if out_eps == 2.0 ** -10 else 0.0
+                tol[t, h] = (np.maximum(out_eps / 2 * np.abs(o[t, h]), least) + A * (2.0 ** -11 + 2 * dx + 2 * (len(w) + 64) * 2.0 ** -23)
+                             + 2.0 ** -29 * np.abs(v).sum(0) / total)
     return o, tol

@@ -77,3 +77,27 @@ def test_a_wide_cap_where_row_tiles_are_searched(dtype, head_dim):
     p = Problem(lens, 4, 2, head_dim, dtype=dtype, seed=3, pad_tokens=3)
     p.options["softcap"] = 1e5
     check(p, f"wide cap searched {dtype} D={head_dim}", max_query_len=300, max_seq_len=256)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("new", NEW)
+@pytest.mark.parametrize("head_dim", [64, 128, 256])
+def test_small_weights_of_many_keys_beside_a_large_one(dtype, head_dim, new):
+    """One key with a value of 0 weighs 2^25.3 times as much as each of 3000 others with values of +-448: the output
+    is theirs, and none of them may be lost."""
+    from oracle import attention as oa
+
+    ctx = 3000
+    p = Problem([(ctx, new)], 8, 2, head_dim, dtype=dtype, seed=61)
+    slots = oa.slots_of(p.table[0], ctx + new, p.block_size, p.num_slots)
+    p.q[:] = 1
+    row = 2 * head_dim
+    p.kc[slots, :row] = 0
+    p.vc[slots, :row] = np.where(np.arange(row) % 3 == 0, 0xFE, 0x7E)  # -448, 448
+    top = slots[ctx - 1]  # the last position that every row sees
+    p.kc[top, :row] = 0x38  # 1.0
+    p.vc[top, :row] = 0
+    p.vs = np.float32(1.0)
+    p.scale = float(np.float32(25.3 * np.log(2.0) / (head_dim * float(p.ks))))
+    got = check(p, f"small weights {dtype} D={head_dim} new={new}", max_query_len=new, max_seq_len=1000)
+    assert np.all(got != 0)
