@@ -87,6 +87,21 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 x, u32x4 y, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
 }
 
+// Whether one of n elements of q (a multiple of 8) is infinite or NaN: all bits of its exponent are set, and the
+// lowest of them added carries into the sign's place.
+template <bool BF16>
+__device__ __forceinline__ bool no_numbers(const uint16_t* q, int n) {
+  constexpr uint32_t exponent = BF16 ? 0x7F807F80u : 0x7C007C00u, lowest = BF16 ? 0x00800080u : 0x04000400u;
+  uint32_t bad = 0;
+#pragma unroll 1
+  for (int i = 0; i < n; i += 8) {
+    const u32x4 v = *reinterpret_cast<const u32x4*>(q + i);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) bad |= ((v[k] & exponent) + lowest) & 0x80008000u;
+  }
+  return bad != 0;
+}
+
 __device__ __forceinline__ float other_half_max(float x) { return __builtin_fmaxf(x, __shfl_xor(x, 32)); }
 
 // Barrier that orders LDS only: loads from the cache stay in flight across it.
@@ -375,7 +390,8 @@ __device__ __forceinline__ void segment(const Segment& sg, Shared<D>& lds) {
   // a negative factor goes into the query, so that the largest raw product is the largest score
   const uint32_t flip = c < 0.0f ? 0x80008000u : 0u;
   c = __builtin_fabsf(c);
-  // (and a factor of 0 too: -inf, a masked score, times 0 would be NaN)
+  // (and a factor of 0 too: -inf, a masked score, times 0 would be NaN; elements that are no numbers, times 0, are
+  // looked at behind the loop)
   const uint32_t keep = c == 0.0f ? 0u : 0xFFFFFFFFu;
   if (c == 0.0f) c = 1.0f;
   const float inv_cap = a.cap > 0.0f ? 1.0f / a.cap : 0.0f;
@@ -532,9 +548,19 @@ __device__ __forceinline__ void segment(const Segment& sg, Shared<D>& lds) {
     }
   }
 
-  const float l = s.l + __shfl_xor(s.l, 32);
+  float l = s.l + __shfl_xor(s.l, 32);
   const AttnArgs& ea = args();
   const int32_t token = token_of(ea, rq, my_row);
+  if (rarely(ea.scale * *ea.ks * kLog2e == 0.0f)) {
+    // (here, and not where the query is read: what stands before the loop moves it, and its time depends on
+    // its address modulo 32 by up to 7 %)
+    bool none = false;
+    if (token >= 0) {
+      const int32_t head = head_of(ea, rq, uniform(lds.share.segment.kv_head), my_row);
+      none = no_numbers<BF16>(ea.q + (int64_t)token * ea.q_ts + (int64_t)head * ea.q_hs, D);
+    }
+    if (none && l > 0.0f) l = __builtin_nanf("");  // a row that sees nothing stays 0
+  }
   if (token >= 0) {
     const Segment& now = lds.share.segment;
     const bool first = uniform(now.first), last = uniform(now.last);
