@@ -23,8 +23,8 @@ CEILING_SRC = "ceiling.hip"
 CEILING_LIB = os.path.join(PKG, "libnvfp4_ceiling.so")
 
 SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "gemm_skinny.hip", "gemm_stream.hip", "kv_cache.hip",
-           "fake_quant.hip", "attention_api.hip", "kv_tables.hip", "kv_attention.hip",
-           "kv_attention_tiled.hip"]
+           "fake_quant.hip", "attention_api.hip", "attention_plan.hip", "kv_tables.hip",
+           "kv_attention.hip", "kv_attention_tiled.hip"]
 
 ARCH = "gfx950"
 

@@ -90,6 +90,16 @@ struct AttnArgs {
   int32_t all_tiles;  // as in the plan
 };
 
+// Workgroups that share a compute unit's registers: what a call is divided among.  More of them keep more
+// loads in flight, as long as their operands fit: 4 KB a step and wavefront with 64 dims, 16 KB with 256.
+constexpr int stream_groups(int head_dim, int rows) {
+  if (head_dim == 64) return 3;
+  if (head_dim == 128) return rows == 16 ? 3 : 2;
+  return 1;
+}
+
+constexpr int kStreamUnit = 128;  // positions of a workgroup's step in the streaming kernel
+
 AttnPlan plan_attention(int64_t tokens, int64_t heads, int64_t kv_heads,
                         int64_t head_dim, int64_t requests, int64_t max_query_len,
                         int64_t max_seq_len);
