@@ -213,6 +213,36 @@ def _rows(t, shape, dtype, device, name):
     return (ts if shape[0] > 1 else shape[1] * shape[2]), (hs if shape[1] > 1 else shape[2])
 
 
+def _refuse_overlap_of_rows(q, q_strides, out, out_strides):
+    """Raise ValueError where ``out [tokens, heads, head_dim]`` shares elements with ``q`` and is not ``q`` itself (the
+    same elements in the same places: an item's rows are read before they are written)."""
+    T, H, D = q.shape
+    if T == 0:
+        return
+    ahead, size = out.data_ptr() - q.data_ptr(), q.element_size()
+    spans = [(T - 1) * ts + (H - 1) * hs + D for ts, hs in (q_strides, out_strides)]
+    if ahead >= spans[0] * size or -ahead >= spans[1] * size or (ahead == 0 and q_strides == out_strides):
+        return
+    if ahead % size == 0:
+        # windows side by side in rows of one pitch (a fused row; head-major storage: heads for tokens)
+        for pitch, inner, n in ((q_strides[0], 1, H), (q_strides[1], 0, T)):
+            if pitch and pitch == out_strides[1 - inner]:
+                widths = [(n - 1) * s[inner] + D for s in (q_strides, out_strides)]
+                begin = (ahead // size) % pitch
+                if max(widths) <= pitch and begin >= widths[0] and begin + widths[1] <= pitch:
+                    return
+        import numpy as np
+
+        t, h = np.arange(T)[:, None], np.arange(H)[None, :]
+        mine = np.unique(t * q_strides[0] + h * q_strides[1])
+        at = ahead // size + (t * out_strides[0] + h * out_strides[1]).ravel()
+        place = np.searchsorted(mine, at)  # the vectors of q before and behind each one of out
+        before, behind = mine[np.maximum(place, 1) - 1], mine[np.minimum(place, len(mine) - 1)]
+        if not ((np.abs(at - before) < D) | (np.abs(at - behind) < D)).any():
+            return
+    raise ValueError("out must be q itself or share no memory with it")
+
+
 @functools.lru_cache(maxsize=1024)
 def _workspace_bytes(*sizes):
     """Workspace of a call of these sizes (a function of them alone)."""
@@ -266,6 +296,7 @@ def _attention(fn_name, q, key_cache, value_cache, key_scale, value_scale, block
         out_ts, out_hs = H * D, D
     else:
         out_ts, out_hs = _rows(out, (T, H, D), q.dtype, dev, "out")
+        _refuse_overlap_of_rows(q, (q_ts, q_hs), out, (out_ts, out_hs))
     W = block_table.shape[1]
     # without a word from the caller: every request has one token at least
     max_query_len = max(1, T - R + 1 if max_query_len is None else int(max_query_len))
@@ -302,7 +333,7 @@ def nvfp4_kv_fp8_attention(q, key_cache, value_cache, key_scale, value_scale, bl
     they were.  ``max_query_len`` and ``max_seq_len`` (bounds of the requests' lengths) only choose how
     the work is divided.  Single tokens in a call with prompts cost as much as 256 rows each over their
     context: many of them over long contexts are faster in a call of their own.  Returns ``out`` in q's
-    type."""
+    type (given, it is ``q`` itself or shares no memory with it)."""
     torch = _base._torch()
 
     def extra(T, R, dev):

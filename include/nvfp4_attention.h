@@ -123,7 +123,7 @@ nvfp4_status nvfp4_kv_block_tables(const int32_t* context_lens, const int32_t* q
  *   doc_start     device, int32[tokens], or NULL; prefix_lens: device, int32[requests], or NULL.
  *   max_query_len, max_seq_len  bounds of the requests' query and key counts, >= 1: they only choose
  *                 how the work is divided (the results of requests above them are right too).
- *   out           device, as q; may not overlap q.
+ *   out           device, as q; q itself with q's strides, or without overlap with it.
  *   workspace     device, 16-byte aligned, at least the bytes that nvfp4_kv_fp8_attention_workspace
  *                 gives for the same arguments; its contents are used within the call only.  Calls
  *                 that may run at the same time need one each.  May be NULL where that gives 0.

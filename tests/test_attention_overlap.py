@@ -1,6 +1,7 @@
-"""Results of nvfp4_kv_block_tables that share memory with its inputs or with one another: the workgroups of the one
-launch read the lengths while others write results, so the binding refuses such calls (CPU: the library
-call is replaced by a recorder; the tensors have memory, and claim to live on the GPU)."""
+"""Results that share memory with inputs or with one another: in nvfp4_kv_block_tables workgroups read the lengths while
+others write results, in the attentions rows are read and written in any order, so the binding refuses
+such calls (CPU: the library call is replaced by a recorder; the tensors have memory, and claim to
+live on the GPU)."""
 
 import os
 
@@ -113,3 +114,100 @@ def test_what_does_not_overlap_is_taken(call):
     slots = _buffer(2 * T).view(dtype=torch.int64)
     call(free_blocks=slots.view(lens.dtype)[6:6], slot_mapping=slots)  # an empty list has no memory
     call(block_table=buf[: R * (W + 3)].view(R, W + 3)[:, :W], free_blocks=buf[2:2])
+
+
+@pytest.fixture
+def attend(monkeypatch):
+    import torch
+
+    seen = []
+    monkeypatch.setattr(at, "_call", lambda device, fn, *args: seen.append(args))
+
+    def make(q, out, which="prompt"):
+        i32, u8 = torch.int32, torch.uint8
+        z = lambda n, dt=i32: torch.zeros(n, dtype=dt)  # noqa: E731
+        a = dict(q=_Dev(q), key_cache=z((32, 128), u8), value_cache=z((32, 128), u8), key_scale=torch.ones(1), value_scale=torch.ones(1),
+                 block_table=z((2, 3)), query_start=z(3), seq_lens=z(2), block_size=16, num_kv_heads=2, max_seq_len=48, out=out)
+        if which == "tree":
+            return nv.nvfp4_kv_fp8_tree_attention(**a, tree_mask=torch.zeros((q.shape[0], 1), dtype=torch.int64))
+        return nv.nvfp4_kv_fp8_attention(**a)
+
+    make.seen = seen
+    return make
+
+
+@pytest.mark.parametrize("which", ["prompt", "tree"])
+def test_an_output_that_overlaps_the_query_is_refused(attend, which):
+    """Rows are read and written by different workgroups in any order: the output is the query itself or elsewhere."""
+    import torch
+
+    tokens, heads, dim = 6, 4, 64
+    n = heads * dim
+    buf = torch.zeros(tokens * n + 8 * n, dtype=torch.bfloat16)
+    q = buf[: tokens * n].view(tokens, heads, dim)
+    for out in (buf[n:][: tokens * n].view(tokens, heads, dim),  # a token further
+                buf[dim:][: tokens * n].view(tokens, heads, dim),  # a head further
+                buf[tokens * n - 8:][: tokens * n].view(tokens, heads, dim),  # the last elements
+                q.transpose(0, 1).reshape(-1)[:0].new_zeros(0).set_(buf.untyped_storage(), 0, (tokens, heads, dim), (dim, tokens * dim, 1))):
+        with pytest.raises(ValueError, match="out"):
+            attend(q, out, which)
+    one = buf[:n].view(1, heads, dim).expand(tokens, heads, dim)  # one token's query for all
+    with pytest.raises(ValueError, match="out"):
+        attend(one, q, which)
+    assert not attend.seen
+
+
+@pytest.mark.parametrize("which", ["prompt", "tree"])
+def test_outputs_beside_the_query_are_taken(attend, which):
+    import torch
+
+    tokens, heads, dim = 6, 4, 64
+    n = heads * dim
+    buf = torch.zeros(tokens * 3 * n, dtype=torch.bfloat16)
+    rows = buf.view(tokens, 3 * heads, dim)
+    q = rows[:, :heads]
+    for out in (q, rows[:, heads:2 * heads], rows[:, 2 * heads:], torch.zeros(tokens, heads, dim, dtype=torch.bfloat16)):
+        assert attend(q, out, which) is out
+    assert attend(rows[:, 2 * heads:], rows[:, :heads], which) is not None  # before the query
+    flat = buf[: 2 * tokens * n]
+    attend(flat[: tokens * n].view(tokens, heads, dim), flat[tokens * n:].view(tokens, heads, dim), which)
+    attend(flat[: tokens * n].view(heads, tokens, dim).transpose(0, 1), flat[tokens * n:].view(heads, tokens, dim).transpose(0, 1), which)
+    head = buf[: tokens * 2 * n].view(heads, 2 * tokens, dim).transpose(0, 1)  # head-major, tokens of both in turn
+    attend(head[:tokens], head[tokens:], which)
+    attend(q[:0], q[:0], which)
+    attend(q[:1], rows[1:2, :heads], which)
+
+
+def test_the_rule_for_rows_against_their_elements():
+    """Random layouts of both tensors in one small buffer, element by element."""
+    import random
+
+    import torch
+
+    rng = random.Random(3)
+    buf = torch.zeros(2000, dtype=torch.bfloat16)
+    D = 8
+    refused = 0
+    for _ in range(3000):
+        T, H = rng.randrange(1, 5), rng.randrange(1, 5)
+
+        def layout():
+            a, b = (T, H) if rng.random() < 0.5 else (H, T)
+            inner = D + rng.choice([0, 0, 8, D])
+            outer = (b - 1) * inner + D + rng.choice([0, 0, 8, 3 * D, b * inner])
+            return rng.choice([(outer, inner) if a == T else (inner, outer), (rng.choice([0, D, 2 * D]), rng.choice([0, D]))])
+
+        x = layout()
+        y = layout() if rng.random() < 0.4 else x
+        at_x, at_y = rng.randrange(40) * 8, rng.randrange(40) * 8 + rng.choice([0, 0, 0, 1, 4])
+        places = [{o + t * ts + h * hs + d for t in range(T) for h in range(H) for d in range(D)} for o, (ts, hs) in ((at_x, x), (at_y, y))]
+        effective = [(ts if T > 1 else H * D, hs if H > 1 else D) for ts, hs in (x, y)]
+        want = bool(places[0] & places[1]) and not (at_x == at_y and effective[0] == effective[1])
+        q, out = (buf.as_strided((T, H, D), (*s, 1), o) for o, s in ((at_x, x), (at_y, y)))
+        if want:
+            refused += 1
+            with pytest.raises(ValueError):
+                at._refuse_overlap_of_rows(q, effective[0], out, effective[1])
+        else:
+            at._refuse_overlap_of_rows(q, effective[0], out, effective[1])
+    assert 300 < refused < 2700
