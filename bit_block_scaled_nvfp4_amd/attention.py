@@ -92,7 +92,7 @@ def _table(t, rows, device, name):
 def _call(device, fn, *args):
     """Run one library call on ``device`` and its current stream, whichever device is current."""
     torch = _base._torch()
-    # the stream's handle without a Stream object: 0.2 us of a call's 10 instead of 4
+    # the stream's handle without a Stream object: 0.05 us instead of 1.8
     raw_stream, index = torch._C._cuda_getCurrentRawStream, device.index
     if torch._C._cuda_getDevice() == index:
         status = fn(*args, raw_stream(index))

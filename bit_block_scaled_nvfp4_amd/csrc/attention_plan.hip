@@ -15,19 +15,21 @@ AttnPlan plan_attention(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t
                         int64_t requests, int64_t max_query_len, int64_t max_seq_len) {
   AttnPlan p{};
   const int64_t group = heads / kv_heads, rows = max_query_len * group;
-  // Short sequences: one launch of a workgroup per item and no join (one token over 500 positions, 256
-  // dims: 16 us a call; shared among workers and joined 20 us), by row tiles of 32 where these all run
-  // at once (37-token prompt, 222 rows: 15 us; tiles of 256 rows 19 us.  64 prompts of 60 tokens, which
-  // do not run at once: 30 us against 18 us).
+  // Short sequences: one launch of a workgroup per item and no join (one token over 500 and 1000 positions,
+  // 256 dims: 14 and 16 us a call, shared among workers and joined 19 us; over 1500 21 and 19 us), by row
+  // tiles of 32 where these all run at once (prompts of 37 and 500 tokens, 24 heads over 4 of 256 dims: 14 and
+  // 28 us, tiles of 256 rows 20 and 46 us.  64 prompts of 60 tokens, which do not run at once: 29 against 16).
   const bool small = max_seq_len <= kShort && requests * kv_heads * ((rows + 31) / 32) <= kComputeUnits;
   if (rows <= 16) {
     p.kernel = AttnKernel::Stream16;
     p.rows = 16;
   } else if (rows <= 96 || small) {
-    // tiles of 32 rows re-read the keys from the caches and decode them again; tiles of 256 leave
-    // wavefronts idle (64 requests x 6001 positions: 96 rows of 256 dims 277 us against 317 us, 48 rows
-    // of 128 dims 219 us against 290 us; 192 rows of 128 dims 553 us against 364 us, 128 rows of 64
-    // dims 287 us against 184 us)
+    // Tiles of 32 rows re-read the keys from the caches and decode them again; tiles of 256 leave
+    // wavefronts idle.  16 requests of up to 6001 positions, 32 against 256 rows: 48 rows of 128 dims 54
+    // and 76 us, 96 rows of 128 and 256 dims 71 and 85, 79 and 102.  64 requests: 48 rows of 128 and 256
+    // dims 217 and 234, 171 and 270; 96 rows of 256 dims 279 and 287, of 128 dims 321 and 250 (where the
+    // device is full, the other side is ahead there already); 128 rows of 64 dims 289 and 184; 192 rows of
+    // 128 and 256 dims (all 6001 long) 938 and 407, 854 and 412.
     p.kernel = AttnKernel::Stream32;
     p.rows = 32;
   } else {
@@ -41,9 +43,14 @@ AttnPlan plan_attention(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t
   const int64_t items = kv_heads * (requests * each < any ? requests * each : any);
   p.row_tiles = (int32_t)(each < kMaxTiles ? each : kMaxTiles);  // (the kernels' strides cover the others)
   if (p.kernel == AttnKernel::Tiled) {
-    // Where the context is most of the work all row tiles cost alike and sharing balances ragged
-    // lengths (64 trees of 192 rows: 355 us; a workgroup per item 386 us).  A prompt's row tiles cost
-    // as much as they see: they are shared only where they are too few to occupy the device.
+    // Where the context is most of the work all row tiles cost alike, and sharing fills the device and
+    // balances ragged lengths (4 trees of 64 over up to 60000: 505 us, a workgroup per item 3475; chunk of 512
+    // over 6000, 32 heads of 128 dims: 121 and 206; 64 trees of 192 rows over up to 6001: 380 and 367).
+    // A prompt's row tiles cost as much as they see; every one of them counts as the whole request here, so
+    // that equal shares are not equal work.  Fresh prompts of fewer than 256 items are shared all the
+    // same, and lose by it (prompts of 500 to 2000 tokens, 24 heads over 4 of 256 dims: 512 65 us against 48,
+    // 1000 94 against 77, 2048 194 against 140; 32 over 8 of 128 dims: 512 75 and 27, 1500 111 and 56;
+    // 8 heads of 64 dims: 2700 55 and 61, 4096 103 and 92).
     const bool deep = 4 * max_query_len <= max_seq_len;
     if (max_seq_len > 256 && items < (deep ? 4 : 1) * kComputeUnits) p.workers = kComputeUnits;
   } else if (max_seq_len > kShort && items < 4 * kComputeUnits) {
@@ -52,7 +59,7 @@ AttnPlan plan_attention(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t
   // A grid of requests by the longest's row tiles is mostly empty where one prompt joins many single tokens,
   // and an empty workgroup takes the room of a full one: the grid counts all requests' row tiles then, and
   // a workgroup finds its own by summing the lengths (24 heads of 256 dims; 63 tokens over 2000 positions and
-  // a prompt of 4096: 1.78 ms by requests, 0.43 so; 255 over 1000 and a prompt of 8192: 6.55 ms, 1.19).
+  // a prompt of 4096: 1.79 ms by requests, 0.39 so; 255 over 1000 and a prompt of 8192: 6.60 ms, 1.19).
   // Where at least half of the grid's places hold a tile, the place says it, with nothing to sum.
   if (p.kernel == AttnKernel::Tiled && p.workers == 0 && requests * each > 2 * any)
     p.all_tiles = (int32_t)(any < kMaxTiles ? any : kMaxTiles);

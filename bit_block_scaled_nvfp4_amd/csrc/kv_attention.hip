@@ -23,8 +23,8 @@
 //
 // Measured (HBM reads at 6.4 TB/s in a plain read kernel, copies at 4.9 TB/s): 64 requests x up to 8000
 // positions, one token each, 4 KV heads x 256 dims, 569 MB: 112 us a call, 5.1 TB/s; 8 KV heads x 128
-// dims, 569 MB: 119 us; 8 x 64 dims, 285 MB: 92 us, 3.1 TB/s.  One request of 100000 positions, 205 MB:
-// 50 us, of which joining takes 7.
+// dims, 569 MB: 122 us; 8 x 64 dims, 285 MB: 91 us, 3.1 TB/s.  One request of 100000 positions, 205 MB:
+// 50 us.
 #include "kv_attention_common.h"
 
 namespace nvfp4 {
@@ -58,10 +58,10 @@ __device__ __forceinline__ T read(const T* p) {
 // A position that is not in the cache reads slot 0 (there is one) and is masked afterwards.  ONCE: the
 // request's rows fit one tile, every line is read by one workgroup once, and the loads do not ask to be
 // kept in the caches -- except those of keys of 64 and 128 dims, whose lines are read in two or more
-// goes (64 x 8000 positions, 128 dims: values kept 131 us, not kept 122 us, nothing kept 131 us; 256
-// dims: 128, 120 and 116 us).  Several row tiles of a request read the same lines at about the same
-// time, and asking for them to be kept pays (16 x 6001 positions, 3 tiles of 128 dims: 71 us, not kept
-// 78 us).
+// goes (64 x up to 8000 positions, 128 dims: 122 us so, keys not kept 127, all kept 138; 64 dims: 94, 105,
+// 90; 256 dims: 118 us so, keys kept 113, all kept 125; one request of 100000 positions, 256 dims: 50, 44,
+// 44).  Several row tiles of a request read the same lines at about the same time, and asking for them to
+// be kept pays (16 x up to 6001 positions, 2 and 3 tiles of 128 dims: 60 and 80 us, not kept 68 and 88 us).
 template <int D, bool ONCE>
 __device__ __forceinline__ void load_keys(const AttnArgs& a, int32_t slot, const uint8_t* kbase, int lane, Keys<D>& c) {
   const int32_t s = slot < 0 ? 0 : slot;

@@ -18,12 +18,12 @@
 // the two after it are on their way from the cache into registers (one was not enough to cover a read
 // of HBM) and the slots of the one after those are looked up; one barrier a tile.
 //
-// Measured (a dense bf16 library product reaches 1.26 PFLOP/s on the same card): 16384-token prompt, 24
-// heads of 256 dims over 4 KV heads, 3.24 ms, 1.02 PFLOP/s (3.54 ms on a card whose product reaches 1.20);
-// 32 heads of 128 dims 0.99, of 64 dims 0.77, of 128 dims with capped scores 0.79 PFLOP/s.  The matrix
-// cores are busy 45 % of the time at 256 dims, LDS has no bank conflicts.  Tiles with half their rows
-// empty take as long as full ones: with one wavefront a SIMD its own chain (operand reads, scores,
-// softmax, output) shows in full.
+// Measured (a dense bf16 library product of 8192^3 reaches 1.24 PFLOP/s on such a card): 16384-token prompt,
+// 24 heads of 256 dims over 4 KV heads, 3.30 ms, 1.00 PFLOP/s; 32 heads of 128 dims 1.00, of 64 dims 0.78,
+// of 128 dims with capped scores 0.77 PFLOP/s.  The matrix cores are busy 45 % of the time at 256 dims, LDS has
+// no bank conflicts.  Tiles with half their rows empty take as long as full ones: with one wavefront a
+// SIMD its own chain (operand reads, scores, softmax, output) shows in full.  The loop's time depends on its
+// address modulo 32 (chunk of 2048 over 30011 with a bias: 964 to 1030 us over the eight places).
 #include "kv_attention_common.h"
 
 namespace nvfp4 {
