@@ -231,14 +231,13 @@ def _refuse_overlap_of_rows(q, q_strides, out, out_strides):
                 begin = (ahead // size) % pitch
                 if max(widths) <= pitch and begin >= widths[0] and begin + widths[1] <= pitch:
                     return
-        import numpy as np
-
-        t, h = np.arange(T)[:, None], np.arange(H)[None, :]
-        mine = np.unique(t * q_strides[0] + h * q_strides[1])
-        at = ahead // size + (t * out_strides[0] + h * out_strides[1]).ravel()
-        place = np.searchsorted(mine, at)  # the vectors of q before and behind each one of out
-        before, behind = mine[np.maximum(place, 1) - 1], mine[np.minimum(place, len(mine) - 1)]
-        if not ((np.abs(at - before) < D) | (np.abs(at - behind) < D)).any():
+        torch = _base._torch()
+        t, h = torch.arange(T, device="cpu")[:, None], torch.arange(H, device="cpu")[None, :]
+        mine = torch.unique(t * q_strides[0] + h * q_strides[1])
+        at = ahead // size + (t * out_strides[0] + h * out_strides[1]).flatten()
+        place = torch.searchsorted(mine, at)  # the vectors of q before and behind each one of out
+        before, behind = mine[(place - 1).clamp(min=0)], mine[place.clamp(max=len(mine) - 1)]
+        if not bool((((at - before).abs() < D) | ((at - behind).abs() < D)).any()):
             return
     raise ValueError("out must be q itself or share no memory with it")
 
