@@ -26,7 +26,20 @@ Entry points (same names as the C ABI):
   query_start, seq_lens, block_size=, num_kv_heads=, ...)`` -> attention of prompts and single tokens
 * ``nvfp4_kv_fp8_tree_attention(..., tree_mask, ...)`` -> attention of trees of drafted tokens
 
-The last three (``include/nvfp4_attention.h``) are in ``attention.py``.
+The last three (``include/nvfp4_attention.h``) are in ``attention.py``, those that follow
+(``include/nvfp4_serving.h``) in ``serving.py``:
+
+* ``nvfp4_qk_norm_rope(q, k, positions, inv_freq, ...)`` -> ``(q, k)`` normed and rotated
+* ``nvfp4_kv_fp8_append(key, value, positions, inv_freq, key_scale, value_scale, key_cache, value_cache,
+  slot_mapping, ...)`` -- norm, rotate and store in one pass
+* ``nvfp4_kv_fp4_append(key, value, positions, inv_freq, key_gscale, value_gscale, key_codes, key_scales,
+  value_codes, value_scales, slot_mapping, ...)`` -- the same into the 4-bit cache
+* ``nvfp4_kv_fp4_load(codes, scales, gscale, slot_mapping, out_dtype)`` -> decoded rows
+* ``nvfp4_kv_fp4_attention(q, key_codes, key_scales, value_codes, value_scales, key_gscale, value_gscale,
+  block_table, query_start, seq_lens, ...)``, ``nvfp4_kv_fp4_tree_attention(..., tree_mask, ...)`` -> attention
+  over the 4-bit cache
+* ``nvfp4_verify_drafted(target_probs, draft_probs, tokens, query_start, accept_u, sample_u)`` ->
+  ``(accepted, tokens)``
 """
 
 from __future__ import annotations
@@ -554,9 +567,18 @@ def nvfp4_kv_fp8_load(cache, scale, slot_mapping=None, out_dtype=None, width=Non
     return out
 
 
-# last: the module builds on the names above
+# last: these modules build on the names above
 from .attention import (  # noqa: E402,F401
     nvfp4_kv_block_tables,
     nvfp4_kv_fp8_attention,
     nvfp4_kv_fp8_tree_attention,
+)
+from .serving import (  # noqa: E402,F401
+    nvfp4_kv_fp4_append,
+    nvfp4_kv_fp4_attention,
+    nvfp4_kv_fp4_load,
+    nvfp4_kv_fp4_tree_attention,
+    nvfp4_kv_fp8_append,
+    nvfp4_qk_norm_rope,
+    nvfp4_verify_drafted,
 )

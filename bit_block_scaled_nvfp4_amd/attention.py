@@ -344,6 +344,20 @@ def nvfp4_kv_fp8_attention(q, key_cache, value_cache, key_scale, value_scale, bl
                       slopes, extra, max_query_len, max_seq_len, out)
 
 
+def _tree_arguments(tree_mask, positions, T, R, dev):
+    """Arguments of the tree attentions' masks."""
+    torch = _base._torch()
+    if tree_mask.dtype != torch.int64 or tree_mask.dim() != 2 or tree_mask.shape[0] != T:
+        raise ValueError(f"tree_mask must be int64 [{T}, words]")
+    words = tree_mask.shape[1]
+    if not 1 <= words <= MAX_TREE_WORDS or (words > 1 and tree_mask.stride(1) != 1):
+        raise ValueError(f"tree_mask must have 1 to {MAX_TREE_WORDS} contiguous words a row")
+    if tree_mask.device != dev:
+        raise ValueError(f"tree_mask must live on {dev}, got {tree_mask.device}")
+    return (tree_mask.data_ptr(), words, _row_pitch(tree_mask, "tree_mask"),
+            None if positions is None else _vector(positions, T, torch.int32, dev, "positions"))
+
+
 def nvfp4_kv_fp8_tree_attention(q, key_cache, value_cache, key_scale, value_scale, block_table,
                                 query_start, seq_lens, tree_mask, *, block_size, num_kv_heads, scale=None,
                                 softcap=0.0, slopes=None, positions=None, max_query_len=None,
@@ -354,19 +368,7 @@ def nvfp4_kv_fp8_tree_attention(q, key_cache, value_cache, key_scale, value_scal
     of word d // 64 for drafted token d, its own bit included).  ``positions`` (int32 ``[tokens]``) are
     the positions that drafted tokens count at in the distance bias (default: context + index).  Other
     arguments as :func:`nvfp4_kv_fp8_attention`."""
-    torch = _base._torch()
-
-    def extra(T, R, dev):
-        if tree_mask.dtype != torch.int64 or tree_mask.dim() != 2 or tree_mask.shape[0] != T:
-            raise ValueError(f"tree_mask must be int64 [{T}, words]")
-        words = tree_mask.shape[1]
-        if not 1 <= words <= MAX_TREE_WORDS or (words > 1 and tree_mask.stride(1) != 1):
-            raise ValueError(f"tree_mask must have 1 to {MAX_TREE_WORDS} contiguous words a row")
-        if tree_mask.device != dev:
-            raise ValueError(f"tree_mask must live on {dev}, got {tree_mask.device}")
-        return (tree_mask.data_ptr(), words, _row_pitch(tree_mask, "tree_mask"),
-                None if positions is None else _vector(positions, T, torch.int32, dev, "positions"))
-
     return _attention("nvfp4_kv_fp8_tree_attention", q, key_cache, value_cache, key_scale, value_scale,
                       block_table, query_start, seq_lens, block_size, num_kv_heads, scale, softcap,
-                      slopes, extra, max_query_len, max_seq_len, out)
+                      slopes, functools.partial(_tree_arguments, tree_mask, positions), max_query_len, max_seq_len,
+                      out)

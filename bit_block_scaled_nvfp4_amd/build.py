@@ -24,7 +24,8 @@ CEILING_LIB = os.path.join(PKG, "libnvfp4_ceiling.so")
 
 SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "gemm_skinny.hip", "gemm_stream.hip", "kv_cache.hip",
            "fake_quant.hip", "attention_api.hip", "attention_plan.hip", "kv_tables.hip",
-           "kv_attention.hip", "kv_attention_tiled.hip"]
+           "kv_attention.hip", "kv_attention_tiled.hip", "kv_attention_fp4.hip", "kv_attention_tiled_fp4.hip",
+           "head_rows.hip", "verify.hip", "serving_api.hip"]
 
 ARCH = "gfx950"
 
@@ -81,7 +82,7 @@ def build(verbose: bool = False, extra_flags: list[str] | None = None) -> str:
         cmds.append([hipcc, *flags, "-c", os.path.join(CSRC, src), "-o", obj])
     ceil_obj = os.path.join(BUILD, os.path.splitext(CEILING_SRC)[0] + ".o")
     cmds.append([hipcc, *flags, "-c", os.path.join(CSRC, CEILING_SRC), "-o", ceil_obj])
-    with ThreadPoolExecutor(max_workers=min(len(cmds), 4)) as ex:
+    with ThreadPoolExecutor(max_workers=min(len(cmds), 8)) as ex:
         list(ex.map(lambda c: _run(c, verbose), cmds))
     for lib, lib_objs in ((LIB, objs), (CEILING_LIB, [ceil_obj])):
         tmp = lib + ".tmp"

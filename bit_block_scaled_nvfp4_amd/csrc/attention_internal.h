@@ -88,6 +88,10 @@ struct AttnArgs {
   FastDiv bs, group;
   float scale, cap;
   int32_t all_tiles;  // as in the plan
+  // the 4-bit cache's block scales; kc and vc are its codes, ks and vs encode-direction global scales, num_slots
+  // its blocks * block_size (cache_ld is not used)
+  const uint8_t* kbs;
+  const uint8_t* vbs;
 };
 
 // Workgroups that share a compute unit's registers: what a call is divided among.  More of them keep more
@@ -98,16 +102,30 @@ constexpr int stream_groups(int head_dim, int rows) {
   return 1;
 }
 
+// The same over the 4-bit cache, whose codes take half the registers.
+constexpr int stream_groups_fp4(int head_dim, int rows) {
+  if (head_dim == 64) return 3;
+  if (head_dim == 128) return rows == 16 ? 3 : 2;
+  return rows == 16 ? 2 : 1;
+}
+
 constexpr int kStreamUnit = 128;  // positions of a workgroup's step in the streaming kernel
 
 AttnPlan plan_attention(int64_t tokens, int64_t heads, int64_t kv_heads,
                         int64_t head_dim, int64_t requests, int64_t max_query_len,
                         int64_t max_seq_len);
 
+// The same for a call over the 4-bit cache.
+AttnPlan plan_attention_fp4(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t requests,
+                            int64_t max_query_len, int64_t max_seq_len);
+
 hipError_t launch_block_tables(const TablesArgs& a, hipStream_t stream);
 // Launch the plan's kernel (and, with workers, the joining kernel).
 hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, int head_dim, bool bf16,
                             hipStream_t stream);
 hipError_t launch_attention_tiled(const AttnArgs& a, int head_dim, bool bf16, hipStream_t stream);
+hipError_t launch_attention_fp4(const AttnArgs& a, const AttnPlan& p, int head_dim, bool bf16,
+                                hipStream_t stream);
+hipError_t launch_attention_tiled_fp4(const AttnArgs& a, int head_dim, bool bf16, hipStream_t stream);
 
 }  // namespace nvfp4

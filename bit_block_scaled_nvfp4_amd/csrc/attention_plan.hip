@@ -9,10 +9,9 @@ namespace {
 constexpr int64_t kMaxTiles = 4096;  // bound of a grid dimension
 constexpr int64_t kShort = 8 * kStreamUnit;  // positions that a workgroup walks over alone
 
-}  // namespace
-
-AttnPlan plan_attention(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
-                        int64_t requests, int64_t max_query_len, int64_t max_seq_len) {
+// `groups`: workgroups that share a compute unit in the streaming kernel.
+AttnPlan plan(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t requests,
+              int64_t max_query_len, int64_t max_seq_len, int (*groups)(int, int)) {
   AttnPlan p{};
   const int64_t group = heads / kv_heads, rows = max_query_len * group;
   // Short sequences: one launch of a workgroup per item and no join (one token over 500 and 1000 positions,
@@ -54,7 +53,7 @@ AttnPlan plan_attention(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t
     const bool deep = 4 * max_query_len <= max_seq_len;
     if (max_seq_len > 256 && items < (deep ? 4 : 1) * kComputeUnits) p.workers = kComputeUnits;
   } else if (max_seq_len > kShort && items < 4 * kComputeUnits) {
-    p.workers = stream_groups((int)head_dim, p.rows) * kComputeUnits;
+    p.workers = groups((int)head_dim, p.rows) * kComputeUnits;
   }
   // A grid of requests by the longest's row tiles is mostly empty where one prompt joins many single tokens,
   // and an empty workgroup takes the room of a full one: the grid counts all requests' row tiles then, and
@@ -66,6 +65,18 @@ AttnPlan plan_attention(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t
   if (p.workers)
     p.workspace = (int64_t)p.workers * (2 * (int64_t)p.rows * (head_dim + 2) + 8) * (int64_t)sizeof(float);
   return p;
+}
+
+}  // namespace
+
+AttnPlan plan_attention(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                        int64_t requests, int64_t max_query_len, int64_t max_seq_len) {
+  return plan(tokens, heads, kv_heads, head_dim, requests, max_query_len, max_seq_len, stream_groups);
+}
+
+AttnPlan plan_attention_fp4(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t requests,
+                            int64_t max_query_len, int64_t max_seq_len) {
+  return plan(tokens, heads, kv_heads, head_dim, requests, max_query_len, max_seq_len, stream_groups_fp4);
 }
 
 }  // namespace nvfp4

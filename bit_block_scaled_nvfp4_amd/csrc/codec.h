@@ -108,23 +108,35 @@ __device__ __forceinline__ uint32_t e2m1_index(float y) {
   return y < 1.0f ? lo : hi;
 }
 
-// Signed E2M1 codes of fl(v[i] * r) for 16 values, packed two per byte with the even element in
+// Signed E2M1 codes of fl(p[i] * r) for 8 values, packed two per byte with the even element in
 // the low nibble.  Each pair goes through the gfx950 conversion v_cvt_scalef32_pk_fp4_f32 at unit
 // scale (the byte it fills is the last operand).  For every binary32 input other than NaN that
 // conversion gives exactly e2m1_index(|y|) with the sign bit of y on top, zeros and subnormals
 // included; RNE is symmetric, so fl(x * r) carries the sign of x and the magnitude fl(|x| * r).
 // A NaN product (0 * inf, only when r is infinite) is the caller's to avoid.
+__device__ __forceinline__ uint32_t e2m1_pack8(const float* p, float r) {
+  uint32_t w = 0u;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, p[0] * r, p[1] * r, 1.0f, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, p[2] * r, p[3] * r, 1.0f, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, p[4] * r, p[5] * r, 1.0f, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, p[6] * r, p[7] * r, 1.0f, 3);
+  return w;
+}
+
 __device__ __forceinline__ void e2m1_pack16(const float (&v)[16], float r, uint32_t (&word)[2]) {
+  word[0] = e2m1_pack8(v, r);
+  word[1] = e2m1_pack8(v + 8, r);
+}
+
+// The same element by element for an infinite r: 0 * inf is NaN, which e2m1_index maps to index 7.
+__device__ __forceinline__ uint32_t e2m1_pack8_wide(const float* p, float r) {
+  uint32_t w = 0u;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const float* p = v + 8 * h;
-    uint32_t w = 0u;
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, p[0] * r, p[1] * r, 1.0f, 0);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, p[2] * r, p[3] * r, 1.0f, 1);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, p[4] * r, p[5] * r, 1.0f, 2);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, p[6] * r, p[7] * r, 1.0f, 3);
-    word[h] = w;
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t code = e2m1_index(fabsf(p[i]) * r) | ((__float_as_uint(p[i]) >> 31) << 3);
+    w |= code << (4 * i);
   }
+  return w;
 }
 
 // Scale code and packed element codes of a block: amax, the E4M3 code of fl(amax * gs6), its
@@ -144,13 +156,8 @@ __device__ __forceinline__ uint32_t encode_codes(const float (&v)[16], float g, 
   if (r < __builtin_inff()) {
     e2m1_pack16(v, r, word);
   } else {
-    word[0] = 0u;
-    word[1] = 0u;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint32_t code = e2m1_index(fabsf(v[i]) * r) | ((__float_as_uint(v[i]) >> 31) << 3);
-      word[i >> 3] |= code << (4 * (i & 7));
-    }
+    word[0] = e2m1_pack8_wide(v, r);
+    word[1] = e2m1_pack8_wide(v + 8, r);
   }
   return sc;
 }
@@ -166,6 +173,15 @@ __device__ __forceinline__ void encode_block(const float (&v)[16], float g, floa
   out.y = word[1];
   *reinterpret_cast<uint2*>(codes + (int64_t)b * 8) = out;
   scales[b] = (uint8_t)sc;
+}
+
+// Four E4M3 codes of fl(p[i] * inv), clamped to +-448 first so that nothing overflows to NaN.
+__device__ __forceinline__ uint32_t e4m3_pack4(const float* p, float inv) {
+  float y[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) y[j] = __builtin_fminf(__builtin_fmaxf(p[j] * inv, -448.0f), 448.0f);
+  const int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
 }
 
 // Exact binary32 value of an E2M1 magnitude index 0..7: {0, 0.5, 1, 1.5, 2, 3, 4, 6}.

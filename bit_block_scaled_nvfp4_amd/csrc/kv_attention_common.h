@@ -1,4 +1,4 @@
-// Device code shared by the attention kernels over the paged FP8 cache (gfx950): which part of the
+// Device code shared by the attention kernels over the paged caches (gfx950): which part of the
 // work a workgroup takes, which positions a query row sees, how scores are capped and biased, and how
 // partial results of one row tile are kept and joined.
 //
@@ -253,17 +253,94 @@ __device__ __forceinline__ int32_t entry_of(const AttnArgs& a, const int32_t* ta
   return table_row[col < last ? col : last];
 }
 
-// Slot of position j, or -1 where it is not in the cache or not below `end`.
-__device__ __forceinline__ int32_t slot_of(const AttnArgs& a, int32_t entry, int32_t end, uint32_t j) {
+// How the cache holds keys and values.
+enum class Cache {
+  Fp8,  // E4M3 codes, a slot's row [kv_heads * head_dim] after another
+  Fp4   // NVFP4: E2M1 codes, two a byte, and an E4M3 scale for each 16; blocks [kv_heads, block_size, head_dim]
+};
+
+// Slot of position j, or -1 where it is not in the cache or not below `end`.  In the 4-bit cache: the number of the
+// KV head's row (blocks * kv_heads * block_size < 2^31).
+template <Cache C = Cache::Fp8>
+__device__ __forceinline__ int32_t slot_of(const AttnArgs& a, int32_t entry, int32_t end, uint32_t j, int32_t kv_head = 0) {
   const uint32_t col = div_of(j, a.bs);
   const int64_t s = (int64_t)entry * a.bs.d + (j - col * a.bs.d);
   const bool there = j < (uint32_t)end && col < (uint32_t)a.table_width && entry >= 0 && s < a.num_slots;
+  if constexpr (C == Cache::Fp4)
+    return there ? (int32_t)(((uint32_t)entry * (uint32_t)a.kv_heads + (uint32_t)kv_head) * a.bs.d + (j - col * a.bs.d)) : -1;
   return there ? (int32_t)s : -1;
+}
+
+// What a key's products and a value's sums are multiplied by: a decode-direction scale, or the inverse of an
+// encode-direction one.
+template <Cache C>
+__device__ __forceinline__ float scale_of(const float* s) {
+  if constexpr (C == Cache::Fp4) return 1.0f / *s;
+  return *s;
 }
 
 // Address of a slot's row: cache_ld < 2^31.
 __device__ __forceinline__ const uint8_t* row_at(const uint8_t* base, int32_t slot, const AttnArgs& a) {
   return base + (uint64_t)(uint32_t)slot * (uint32_t)a.cache_ld;
+}
+
+// ---- 4-bit codes ----------------------------------------------------------------------------
+//
+// A code times its block's scale has at most 2 + 4 significant bits and lies in [2^-10, 2880]: exact in FP16 and
+// in BF16.  Scale bytes are taken as magnitudes: bit 7 is not looked at, and 0x7F, which the encoder does not
+// write, counts as 480, the next number of the grid.  So whatever the cache holds where nothing was written is
+// finite, and masked by a weight of 0.
+
+// Scale bytes 0 and 1 (or 2 and 3) of w as FP16 times 2^-8: the byte's fields stand 7 bits up in FP16's, whose exponent
+// counts from 15 and not from 7.
+template <int PAIR>
+__device__ __forceinline__ f16x2 scale_pair(uint32_t w) {
+  const uint32_t two = __builtin_amdgcn_perm(0u, w, PAIR ? 0x0C030C02u : 0x0C010C00u);
+  return __builtin_bit_cast(f16x2, (two & 0x007F007Fu) << 7);
+}
+
+// Codes 2 B and 2 B + 1 of w, times 2^8 (what scale_pair lacks).
+template <int B>
+__device__ __forceinline__ f16x2 two_codes(uint32_t w) {
+  return __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 256.0f, B));
+}
+
+template <int B>
+__device__ __forceinline__ uint32_t two_f16(uint32_t w, f16x2 scales) {
+  return __builtin_bit_cast(uint32_t, two_codes<B>(w) * scales);
+}
+
+// The same in BF16, which has no packed product: in FP32, whose upper half it is.  `scale`: byte << 20 as FP32, the
+// scale times 2^-120.
+template <int B>
+__device__ __forceinline__ uint32_t two_bf16(uint32_t w, float scale) {
+  const f32x2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 0x1p120f, B);
+  return __builtin_amdgcn_perm(__float_as_uint(v.y * scale), __float_as_uint(v.x * scale), 0x07060302u);
+}
+
+// Eight codes of a key in the query's type; `byte`: which of the bytes of `scales` is their block's.
+template <bool BF16>
+__device__ __forceinline__ u32x4 decode_key8(uint32_t w, uint32_t scales, int byte) {
+  if constexpr (BF16) {
+    const float s = __uint_as_float((scales >> (8 * byte) & 0x7Fu) << 20);
+    return u32x4{two_bf16<0>(w, s), two_bf16<1>(w, s), two_bf16<2>(w, s), two_bf16<3>(w, s)};
+  }
+  const f16x2 two = byte & 2 ? scale_pair<1>(scales) : scale_pair<0>(scales);
+  const f16x2 s = byte & 1 ? f16x2{two[1], two[1]} : f16x2{two[0], two[0]};
+  return u32x4{two_f16<0>(w, s), two_f16<1>(w, s), two_f16<2>(w, s), two_f16<3>(w, s)};
+}
+
+// Codes of the same 8 dims of two keys, put together by dim: byte b of `even` holds dim 2 b of both keys, of `odd`
+// dim 2 b + 1.
+__device__ __forceinline__ void pair_keys(uint32_t k0, uint32_t k1, uint32_t& even, uint32_t& odd) {
+  constexpr uint32_t low = 0x0F0F0F0Fu;
+  even = (k0 & low) | ((k1 << 4) & ~low);
+  odd = ((k0 >> 4) & low) | (k1 & ~low);
+}
+
+// Scale bytes of two keys (in the low byte of each) as scale_pair gives them.
+__device__ __forceinline__ f16x2 scales_of_keys(uint32_t s0, uint32_t s1) {
+  return __builtin_bit_cast(f16x2, ((s0 | s1 << 16) & 0x007F007Fu) << 7);
 }
 
 // Non-zero where one of the four codes is NaN (0x7F or 0xFF).

@@ -1,0 +1,11 @@
+// The streaming kernels over the 4-bit cache, and the launch of its attentions.
+#include "kv_attention_stream.h"
+
+namespace nvfp4 {
+
+hipError_t launch_attention_fp4(const AttnArgs& a, const AttnPlan& p, int head_dim, bool bf16,
+                                hipStream_t stream) {
+  return launch_any<attn::Cache::Fp4>(a, p, head_dim, bf16, stream);
+}
+
+}  // namespace nvfp4

@@ -66,14 +66,7 @@ __global__ void __launch_bounds__(kThreads) kv_store_kernel(KvStoreArgs a) {
   const float inv = 1.0f / *a.scale[z];  // correctly rounded (built with IEEE division)
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float y[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = __builtin_fminf(__builtin_fmaxf(v[4 * i + j] * inv, -448.0f), 448.0f);
-    int p = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
-    p = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], p, true);
-    w[i] = (uint32_t)p;
-  }
+  for (int i = 0; i < 4; ++i) w[i] = e4m3_pack4(v + 4 * i, inv);
   if (slot < 0) return;
   u32x4 o;
   o.x = w[0];

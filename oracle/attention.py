@@ -70,9 +70,10 @@ def slots_of(table_row, length, block_size, num_slots):
 
 def attention(q, key_cache, value_cache, key_scale, value_scale, block_table, query_start, seq_lens,
               block_size, kv_heads, scale, softcap=0.0, slopes=None, doc_start=None, prefix_lens=None,
-              tree=None, positions=None, out=None, out_eps=0.0):
+              tree=None, positions=None, out=None, out_eps=0.0, decode=_decode):
     """``(out, tolerance)`` in binary64.  ``tree``: bool ``[tokens, drafted]`` (drafted trees), else
-    prompts.  ``out``: initial contents, kept where no request owns a row.  The tolerance of an element
+    prompts.  ``decode``: ``(cache rows, scale)`` to values, the FP8 cache's unless given.  ``out``: initial
+    contents, kept where no request owns a row.  The tolerance of an element
     counts the roundings of an FP32 computation whose exponentials are rounded to FP16 (half steps
     2^-24 and 2^-11; below 2^-14 an absolute 2^-25, where a row's largest weight is 2^4 at least) and whose
     result is rounded with relative step ``out_eps``:
@@ -111,8 +112,8 @@ def attention(q, key_cache, value_cache, key_scale, value_scale, block_table, qu
                     kpos[ctx + d] = positions[t0 + d]
         for h in range(H):
             cols = slice((h // G) * D, (h // G) * D + D)
-            K = _decode(key_cache[np.maximum(slot, 0), cols], key_scale)
-            V = _decode(value_cache[np.maximum(slot, 0), cols], value_scale)
+            K = decode(key_cache[np.maximum(slot, 0), cols], key_scale)
+            V = decode(value_cache[np.maximum(slot, 0), cols], value_scale)
             for i in range(n):
                 t, p = t0 + i, ctx + i
                 if tree is not None:
