@@ -7,6 +7,8 @@ namespace {
 
 bool valid_dtype(int d) { return d == NVFP4_F32 || d == NVFP4_BF16 || d == NVFP4_F16; }
 
+constexpr int64_t kMaxStride = int64_t(1) << 32;  // bytes from one head vector to the next
+
 int64_t bytes_of(int d) { return d == NVFP4_F32 ? 4 : 2; }
 
 // Head vectors of one kind, as a call gives them.
@@ -29,6 +31,7 @@ struct Turn {
 nvfp4_status check_vectors(const Vectors& v, int dtype, int64_t tokens, int64_t head_dim, bool out) {
   const int64_t eb = bytes_of(dtype);
   if (!span_fits(tokens, v.heads, head_dim, v.ts, v.hs)) return NVFP4_ESHAPE;
+  if ((tokens > 1 && v.ts * eb >= kMaxStride) || (v.heads > 1 && v.hs * eb >= kMaxStride)) return NVFP4_ESHAPE;
   if (out && !distinct(tokens, v.heads, head_dim, v.ts, v.hs)) return NVFP4_ESHAPE;
   if (!aligned(v.x, 16) || (tokens > 1 && v.ts * eb % 16) || (v.heads > 1 && v.hs * eb % 16)) return NVFP4_EALIGN;
   return NVFP4_OK;
@@ -54,10 +57,10 @@ nvfp4::HeadGroup group_of(const Vectors& v, int dtype, int64_t tokens, const voi
   nvfp4::HeadGroup g{};
   const int64_t eb = bytes_of(dtype);
   g.src = static_cast<const uint8_t*>(v.x);
-  g.ts = tokens > 1 ? v.ts * eb : 0;
-  g.hs = v.heads > 1 ? v.hs * eb : 0;
+  g.ts = (uint32_t)(tokens > 1 ? v.ts * eb : 0);
+  g.hs = (uint32_t)(v.heads > 1 ? v.hs * eb : 0);
   g.weight = static_cast<const uint8_t*>(weight);
-  g.heads = (int32_t)v.heads;
+  g.heads = nvfp4::make_fast_div((uint32_t)v.heads);
   g.turned = turned ? 1 : 0;
   return g;
 }
@@ -255,10 +258,11 @@ nvfp4_status nvfp4_kv_fp4_load(const uint8_t* codes, const uint8_t* scales, int6
   a.slots = slot_mapping;
   a.out = static_cast<uint8_t*>(out);
   a.num_slots = num_blocks * block_size;
-  a.head_dim = (int32_t)head_dim;
+  a.tokens = tokens;
+  a.head_bits = head_dim == 64 ? 6 : (head_dim == 128 ? 7 : 8);
   a.kv_heads = (int32_t)kv_heads;
   a.bs = nvfp4::make_fast_div((uint32_t)block_size);
-  return device_status(nvfp4::launch_fp4_load(a, out_dtype == NVFP4_BF16, tokens, reinterpret_cast<hipStream_t>(stream)));
+  return device_status(nvfp4::launch_fp4_load(a, out_dtype == NVFP4_BF16, reinterpret_cast<hipStream_t>(stream)));
 }
 
 nvfp4_status nvfp4_kv_fp4_attention(

@@ -11,15 +11,15 @@ namespace nvfp4 {
 
 // Head vectors of one kind: queries, keys or values.
 struct HeadGroup {
-  const uint8_t* src;
-  int64_t ts, hs;      // bytes
+  const uint8_t* src;  // or null: no such vectors
+  uint32_t ts, hs;     // bytes
   uint8_t* out;        // same type: rows with strides of their own
-  int64_t out_ts, out_hs;
+  uint32_t out_ts, out_hs;
   const uint8_t* weight;  // or null: no norm
   const float* scale;  // of a cache: decode direction (FP8), encode direction (4 bits)
   uint8_t* cache;      // codes
   uint8_t* cache_scales;
-  int32_t heads;
+  FastDiv heads;
   int32_t turned;      // rotated
 };
 
@@ -30,12 +30,11 @@ struct HeadArgs {
   const int32_t* positions;
   const float* inv_freq;
   const int64_t* slots;  // caches: null for slot t
-  double eps, offset;
+  double eps, offset, per_dim;  // per_dim: 1 / head_dim
   int64_t num_slots, cache_ld;
   int32_t tokens, head_dim, num_freq, interleaved;
   int32_t weight_dtype;
   int32_t block_tokens;  // tokens of a workgroup
-  FastDiv all_heads;     // of both groups
   FastDiv bs;
 };
 
@@ -47,13 +46,14 @@ struct Fp4LoadArgs {
   const float* g;
   const int64_t* slots;
   uint8_t* out;
-  int64_t num_slots, pieces;
-  int32_t head_dim;
+  int64_t num_slots, tokens;
+  int32_t head_bits;  // log2 of head_dim
   int32_t kv_heads;
+  int32_t pieces;     // of 16 bytes of the result, a token
   FastDiv bs;
 };
 
-hipError_t launch_fp4_load(const Fp4LoadArgs& a, bool bf16_out, int64_t tokens, hipStream_t stream);
+hipError_t launch_fp4_load(Fp4LoadArgs a, bool bf16_out, hipStream_t stream);
 
 constexpr int kVerifyChunk = 4096;  // tokens of the vocabulary that a workgroup sums
 

@@ -78,12 +78,19 @@ def declare(lib: ctypes.CDLL) -> None:
 # ---- head vectors -----------------------------------------------------------------------------
 
 
-def _heads(t, name, device=None, tokens=None, head_dim=None, dtype=None):
+def _strides(t, shape, dtype, device, name):
     """Check ``t [tokens, heads, head_dim]``; returns its token and head strides."""
-    if t.dim() != 3:
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be 3-D [tokens, heads, head_dim], got {list(shape)}")
+    if t.shape == shape and t.dtype is dtype and t.device == device:
+        ts, hs, one = t.stride()
+        if one == 1:
+            T, H, D = shape
+            # (the stride of a dimension of one element addresses nothing)
+            return (ts if T > 1 else H * D, hs if H > 1 else D)
+    elif t.dim() != 3:
         raise ValueError(f"{name} must be 3-D [tokens, heads, head_dim], got {list(t.shape)}")
-    want = (t.shape[0] if tokens is None else tokens, t.shape[1], t.shape[2] if head_dim is None else head_dim)
-    return _rows(t, want, t.dtype if dtype is None else dtype, t.device if device is None else device, name)
+    return _rows(t, tuple(shape), dtype, device, name)
 
 
 def _meet(a, b):
@@ -111,22 +118,20 @@ def _meet(a, b):
                  | ((its >= behind) & (its < behind + w))).any())
 
 
-def _turn(positions, inv_freq, tokens, head_dim, device, eps, weight_offset, interleaved, step=8):
+def _turn(positions, inv_freq, tokens, head_dim, device, interleaved, step, torch):
     """Arguments of the rotation: positions, frequencies, their number, the flag."""
-    torch = _base._torch()
-    if (positions is None) != (inv_freq is None):
-        raise ValueError("positions and inv_freq come together")
-    if interleaved not in (False, True):
+    if interleaved is not False and interleaved is not True and interleaved not in (0, 1):
         raise ValueError(f"interleaved must be True or False, got {interleaved!r}")
-    if positions is None:
-        return None, None, 0, int(interleaved), float(eps), float(weight_offset)
-    n = inv_freq.shape[0] if inv_freq.dim() == 1 else -1
-    if n < 0 or n % step or 2 * n > head_dim:
-        raise ValueError(f"inv_freq must hold a multiple of {step} values, at most {head_dim // 2}, "
-                         f"got shape {list(inv_freq.shape)}")
+    if positions is None or inv_freq is None:
+        if positions is not None or inv_freq is not None:
+            raise ValueError("positions and inv_freq come together")
+        return None, None, 0, interleaved
+    shape = inv_freq.shape
+    if len(shape) != 1 or shape[0] % step or 2 * shape[0] > head_dim:
+        raise ValueError(f"inv_freq must hold a multiple of {step} values, at most {head_dim // 2}, got shape {list(shape)}")
+    n = shape[0]
     return (_vector(positions, tokens, torch.int32, device, "positions"),
-            _vector(inv_freq, n, torch.float32, device, "inv_freq"), n, int(interleaved), float(eps),
-            float(weight_offset))
+            _vector(inv_freq, n, torch.float32, device, "inv_freq"), n, interleaved)
 
 
 def _weight(t, head_dim, device, name):
@@ -136,13 +141,10 @@ def _weight(t, head_dim, device, name):
     return _vector(t, head_dim, t.dtype, device, name), _base._dtype_code(t.dtype)
 
 
-def _span(t, strides):
-    """Byte range ``(begin, end)`` of head vectors."""
-    T, H, D = t.shape
-    if not T * H * D:
-        return 0, 0
-    p = t.data_ptr()
-    return p, p + t.element_size() * ((T - 1) * strides[0] + (H - 1) * strides[1] + D)
+def _extent(shape, strides, size):
+    """Bytes from the first to past the last element of head vectors."""
+    T, H, D = shape
+    return size * ((T - 1) * strides[0] + (H - 1) * strides[1] + D) if T and H else 0
 
 
 def nvfp4_qk_norm_rope(q, k=None, positions=None, inv_freq=None, *, q_weight=None, k_weight=None, eps=1e-6,
@@ -158,46 +160,54 @@ def nvfp4_qk_norm_rope(q, k=None, positions=None, inv_freq=None, *, q_weight=Non
     the inputs' type; each may be given, and be its own input (in place)."""
     torch = _base._torch()
     lib = _lib()
-    dev = _cuda(q, "q")
-    q_strides = _heads(q, "q")
-    T, H, D = q.shape
+    dev, shape, dtype = _cuda(q, "q"), q.shape, q.dtype
+    q_strides = _strides(q, shape, dtype, dev, "q")
+    T, H, D = shape
     if H < 1 or H > 1024:
         raise ValueError(f"q must have 1 to 1024 heads, got {H}")
     if D % 16 or not 16 <= D <= MAX_HEAD_DIM:
         raise ValueError(f"head_dim must be a multiple of 16 up to {MAX_HEAD_DIM}, got {D}")
-    code = _base._dtype_code(q.dtype)
-    Hk, k_strides = 0, (0, 0)
-    if k is not None:
-        k_strides = _heads(k, "k", dev, T, D, q.dtype)
-        Hk = k.shape[1]
-        if Hk > 1024:
-            raise ValueError(f"k must have at most 1024 heads, got {Hk}")
-    elif k_out is not None or k_weight is not None:
-        raise ValueError("k_out and k_weight come with k")
-    p, f, n, pairs, eps, offset = _turn(positions, inv_freq, T, D, dev, eps, weight_offset, interleaved)
+    code = _base._dtype_code(dtype)
+    p, f, n, pairs = _turn(positions, inv_freq, T, D, dev, interleaved, 8, torch)
     qw, wt = _weight(q_weight, D, dev, "q_weight")
     kw, kt = _weight(k_weight, D, dev, "k_weight")
     if q_weight is None:
         wt = kt
     elif k_weight is not None and kt != wt:
         raise ValueError("q_weight and k_weight must have one type")
-    new_q, new_k = q_out is None, k_out is None
-    if new_q:
-        q_out, qo_strides = torch.empty((T, H, D), dtype=q.dtype, device=dev), (H * D, D)
-    else:
-        qo_strides = _rows(q_out, (T, H, D), q.dtype, dev, "q_out")
-    ko_strides = (0, 0)
+    qp, size = q.data_ptr(), 4 if code == _base.NVFP4_F32 else 2
+    kp, ko, Hk, k_strides, ko_strides, ko_end, k_end = None, None, 0, (0, 0), (0, 0), 0, 0
     if k is not None:
-        if new_k:
-            k_out, ko_strides = torch.empty((T, Hk, D), dtype=q.dtype, device=dev), (Hk * D, D)
+        k_shape = k.shape
+        if len(k_shape) != 3 or k_shape[0] != T or k_shape[2] != D or k_shape[1] > 1024:
+            raise ValueError(f"k must have shape [{T}, heads up to 1024, {D}], got {list(k_shape)}")
+        Hk = k_shape[1]
+        k_strides = _strides(k, k_shape, dtype, dev, "k")
+        kp = k.data_ptr()
+        if k_out is None:
+            k_out, ko_strides = torch.empty(k_shape, dtype=dtype, device=dev), (Hk * D, D)
+            ko = k_out.data_ptr()
         else:
-            ko_strides = _rows(k_out, (T, Hk, D), q.dtype, dev, "k_out")
-    if not (new_q and new_k):
-        _refuse_meeting(q, q_strides, k, k_strides, None if new_q else q_out, qo_strides, None if new_k else k_out,
-                        ko_strides)
-    _call(dev, lib.nvfp4_qk_norm_rope, q.data_ptr(), H, *q_strides, None if k is None else k.data_ptr(), Hk, *k_strides,
-          code, T, D, p, f, n, pairs, qw, kw, wt, eps, offset, q_out.data_ptr(), *qo_strides,
-          None if k is None else k_out.data_ptr(), *ko_strides)
+            ko_strides = _strides(k_out, k_shape, dtype, dev, "k_out")
+            ko = k_out.data_ptr()
+            ko_end = ko + _extent(k_shape, ko_strides, size)
+        k_end = kp + _extent(k_shape, k_strides, size)
+    elif k_out is not None or k_weight is not None:
+        raise ValueError("k_out and k_weight come with k")
+    q_end = qp + _extent(shape, q_strides, size)
+    if q_out is None:
+        q_out, qo_strides = torch.empty(shape, dtype=dtype, device=dev), (H * D, D)
+        qo, qo_end = q_out.data_ptr(), 0
+    else:
+        qo_strides = _strides(q_out, shape, dtype, dev, "q_out")
+        qo = q_out.data_ptr()
+        qo_end = qo + _extent(shape, qo_strides, size)
+    # (an output made here has no end: it meets nothing)
+    if ((qo < q_end and qp < qo_end) or (ko_end and (kp < ko_end and ko < k_end or qp < ko_end and ko < q_end or ko < qo_end and qo < ko_end))
+            or (kp is not None and kp < qo_end and qo < k_end)):
+        _refuse_meeting(q, q_strides, k, k_strides, q_out if qo_end else None, qo_strides, k_out if ko_end else None, ko_strides)
+    _call(dev, lib.nvfp4_qk_norm_rope, qp, H, *q_strides, kp, Hk, *k_strides, code, T, D, p, f, n, pairs, qw, kw, wt, eps,
+          weight_offset, qo, *qo_strides, ko, *ko_strides)
     return q_out, k_out
 
 
@@ -206,10 +216,6 @@ def _refuse_meeting(q, q_strides, k, k_strides, q_out, qo_strides, k_out, ko_str
     given = [(x, s, name, mine) for x, s, name, mine in ((q, q_strides, "q", 0), (k, k_strides, "k", 1),
                                                          (q_out, qo_strides, "q_out", 0), (k_out, ko_strides, "k_out", 1))
              if x is not None]
-    # ranges that are disjoint, each before the next, share nothing
-    spans = sorted(_span(x, s) for x, s, _, _ in given)
-    if all(a[1] <= b[0] for a, b in zip(spans, spans[1:])):
-        return
     as_bytes = [(x.data_ptr(), *x.shape[:2], x.shape[2] * x.element_size(), *(n * x.element_size() for n in s))
                 for x, s, _, _ in given]
     for i, (x, s, name, mine) in enumerate(given):
@@ -228,10 +234,7 @@ def _refuse_meeting(q, q_strides, k, k_strides, q_out, qo_strides, k_out, ko_str
 
 def _refuse_ranges(outs, ins):
     """Raise ValueError where a byte range ``(name, begin, end)`` of ``outs`` meets another one or one of ``ins``."""
-    starts = sorted(r[1] for r in (*outs, *ins) if r[2] > r[1])
-    ends = sorted(r[2] for r in (*outs, *ins) if r[2] > r[1])
-    if not any(map(operator.gt, ends, starts[1:])):
-        return
+    ins = list(ins)
     for i, (name, p, e) in enumerate(outs):
         for other, q, f in (*outs[:i], *ins):
             if p < f and q < e and e > p and f > q:
@@ -239,32 +242,31 @@ def _refuse_ranges(outs, ins):
 
 
 def _append(key, value, positions, inv_freq, k_scale, v_scale, scale_names, slots, k_weight, eps, weight_offset,
-            interleaved, step):
+            interleaved, step, torch):
     """What both appends check; returns the common arguments, the device, sizes and the byte ranges read."""
-    torch = _base._torch()
-    dev = _cuda(key, "key")
-    k_strides = _heads(key, "key")
-    T, Hk, D = key.shape
+    dev, shape, dtype = _cuda(key, "key"), key.shape, key.dtype
+    k_strides = _strides(key, shape, dtype, dev, "key")
+    T, Hk, D = shape
     if Hk < 1 or Hk > 1024:
         raise ValueError(f"key must have 1 to 1024 heads, got {Hk}")
     if D != 64 and D != 128 and D != 256:
         raise ValueError(f"head_dim must be 64, 128 or 256, got {D}")
-    code = _base._dtype_code(key.dtype)
-    if value.dim() != 3:
-        raise ValueError("value must be 3-D [tokens, heads, head_dim]")
-    v_strides = _rows(value, (T, Hk, D), key.dtype, dev, "value")
-    p, f, n, pairs, eps, offset = _turn(positions, inv_freq, T, D, dev, eps, weight_offset, interleaved, step)
+    code = _base._dtype_code(dtype)
+    v_strides = _strides(value, shape, dtype, dev, "value")
+    p, f, n, pairs = _turn(positions, inv_freq, T, D, dev, interleaved, step, torch)
     kw, wt = _weight(k_weight, D, dev, "k_weight")
     for s, name in ((k_scale, scale_names[0]), (v_scale, scale_names[1])):
-        if s.dtype != torch.float32 or s.numel() != 1 or s.device != dev:
+        if s.dtype is not torch.float32 or s.numel() != 1 or s.device != dev:
             raise ValueError(f"{name} must be one float32 value on {dev}")
     sm = None if slots is None else _vector(slots, T, torch.int64, dev, "slot_mapping")
-    args = (key.data_ptr(), value.data_ptr(), code, T, Hk, D, *k_strides, *v_strides, p, f, n, pairs, kw, wt, eps, offset,
+    k, v, size = key.data_ptr(), value.data_ptr(), 4 if code == _base.NVFP4_F32 else 2
+    args = (k, v, code, T, Hk, D, *k_strides, *v_strides, p, f, n, pairs, kw, wt, eps, weight_offset,
             k_scale.data_ptr(), v_scale.data_ptr(), sm)
-    ins = [("key", *_span(key, k_strides)), ("value", *_span(value, v_strides))]
-    if sm is not None:
-        ins.append(("slot_mapping", sm, sm + 8 * T))
-    return args, dev, (T, Hk, D), ins
+    ke, ve = k + _extent(shape, k_strides, size), v + _extent(shape, v_strides, size)
+    if k < ve and v < ke:  # (of one fused row: one range)
+        k, ke = min(k, v), max(ke, ve)
+        v = ve = k
+    return args, dev, (T, Hk, D), (k, v, sm or 0), (ke, ve, sm + 8 * T if sm else 0)
 
 
 def nvfp4_kv_fp8_append(key, value, positions, inv_freq, key_scale, value_scale, key_cache, value_cache,
@@ -278,47 +280,53 @@ def nvfp4_kv_fp8_append(key, value, positions, inv_freq, key_scale, value_scale,
     with an input or the other cache."""
     torch = _base._torch()
     lib = _lib()
-    args, dev, (T, Hk, D), ins = _append(key, value, positions, inv_freq, key_scale, value_scale,
-                                         ("key_scale", "value_scale"), slot_mapping, k_weight, eps, weight_offset,
-                                         interleaved, 8)
-    width = Hk * D
+    args, dev, (T, Hk, D), begin, end = _append(key, value, positions, inv_freq, key_scale, value_scale,
+                                                ("key_scale", "value_scale"), slot_mapping, k_weight, eps, weight_offset,
+                                                interleaved, 8, torch)
+    width, shape, strides = Hk * D, key_cache.shape, key_cache.stride()
     for c, name in ((key_cache, "key_cache"), (value_cache, "value_cache")):
-        if c.dtype != torch.uint8 or c.dim() != 2 or c.shape[1] < width or c.stride(1) != 1:
+        if c.dtype is not torch.uint8 or c.dim() != 2 or c.shape[1] < width or c.stride(1) != 1:
             raise ValueError(f"{name} must be uint8 [num_slots, >= {width}] with contiguous rows")
         if c.device != dev:
             raise ValueError(f"{name} must live on {dev}, got {c.device}")
-    slots = key_cache.shape[0]
-    if value_cache.shape[0] != slots or (slots > 1 and value_cache.stride(0) != key_cache.stride(0)):
+    slots = shape[0]
+    if value_cache.shape[0] != slots or (slots > 1 and value_cache.stride(0) != strides[0]):
         raise ValueError("value_cache must have key_cache's slots and row pitch")
-    ld = key_cache.stride(0) if slots > 1 else max(width, key_cache.shape[1] // 16 * 16)
+    ld = strides[0] if slots > 1 else max(width, shape[1] // 16 * 16)
     kp, vp = key_cache.data_ptr(), value_cache.data_ptr()
     extent = (slots - 1) * ld + width if slots else 0
     if kp < vp + extent and vp < kp + extent and not width <= (vp - kp) % ld <= ld - width:
         raise ValueError("value_cache must not share memory with key_cache")
-    for c, p in (("key_cache", kp), ("value_cache", vp)):
-        _refuse_ranges([(c, p, p + extent)], ins)
+    for i, e in zip(begin, end):
+        if kp < e and i < kp + extent or vp < e and i < vp + extent:
+            _refuse_ranges([("key_cache", kp, kp + extent)], [("key, value or slot_mapping", i, e)])
+            _refuse_ranges([("value_cache", vp, vp + extent)], [("key, value or slot_mapping", i, e)])
     _call(dev, lib.nvfp4_kv_fp8_append, *args, kp, vp, slots, ld)
 
 
-def _cache4(codes, scales, dev, names, like=None):
-    """Check one tensor of the 4-bit cache and its scales; returns ``(num_blocks, kv_heads, block_size, head_dim)``."""
-    torch = _base._torch()
-    for t, name in ((codes, names[0]), (scales, names[1])):
-        if t.dtype != torch.uint8 or t.dim() != 4:
-            raise ValueError(f"{name} must be uint8 [num_blocks, kv_heads, block_size, ...], got {t.dtype} {list(t.shape)}")
-        if t.device != dev:
-            raise ValueError(f"{name} must live on {dev}, got {t.device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    B, Hk, bs, half = codes.shape
+def _cache4(codes, scales, dev, names, torch, like=None):
+    """Check one tensor of the 4-bit cache and its scales; returns ``(num_blocks, kv_heads, block_size, head_dim)``.
+    ``like``: what this gave for the keys."""
+    u8, shape = torch.uint8, codes.shape
+    if not (codes.dtype is u8 and scales.dtype is u8 and len(shape) == 4 and codes.device == dev and scales.device == dev
+            and codes.is_contiguous() and scales.is_contiguous()):
+        for t, name in ((codes, names[0]), (scales, names[1])):
+            if t.dtype != u8 or t.dim() != 4:
+                raise ValueError(f"{name} must be uint8 [num_blocks, kv_heads, block_size, ...], got {t.dtype} {list(t.shape)}")
+            if t.device != dev:
+                raise ValueError(f"{name} must live on {dev}, got {t.device}")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+    B, Hk, bs, half = shape
     if scales.shape != (B, Hk, bs, half // 8) or half % 8:
         raise ValueError(f"{names[1]} must have shape {[B, Hk, bs, half // 8]}, got {list(scales.shape)}")
-    if half not in (32, 64, 128):
-        raise ValueError(f"head_dim must be 64, 128 or 256, got {2 * half}")
-    if Hk < 1 or not 1 <= bs <= 1 << 24 or B * Hk * bs >= 2 ** 31:
-        raise ValueError(f"{names[0]} must have KV heads, blocks of 1 to 2^24 slots and fewer than 2^31 rows")
     got = (B, Hk, bs, 2 * half)
-    if like is not None and got != like:
+    if like is None:
+        if half not in (32, 64, 128):
+            raise ValueError(f"head_dim must be 64, 128 or 256, got {2 * half}")
+        if Hk < 1 or not 1 <= bs <= 1 << 24 or B * Hk * bs >= 2 ** 31:
+            raise ValueError(f"{names[0]} must have KV heads, blocks of 1 to 2^24 slots and fewer than 2^31 rows")
+    elif got != like:
         raise ValueError(f"{names[0]} must have the keys' shape")
     return got
 
@@ -334,19 +342,24 @@ def nvfp4_kv_fp4_append(key, value, positions, inv_freq, key_gscale, value_gscal
     ``slot_mapping`` (int64 ``[tokens]``; None: token t in slot t) counts ``block * block_size + place``, as
     :func:`nvfp4_kv_block_tables` gives it; slots outside the cache are skipped.  Without ``interleaved``, ``inv_freq``
     holds a multiple of 16 values.  Other arguments as :func:`nvfp4_kv_fp8_append`."""
+    torch = _base._torch()
     lib = _lib()
-    args, dev, (T, Hk, D), ins = _append(key, value, positions, inv_freq, key_gscale, value_gscale,
-                                         ("key_gscale", "value_gscale"), slot_mapping, k_weight, eps, weight_offset,
-                                         interleaved, 8 if interleaved else 16)
-    shape = _cache4(key_codes, key_scales, dev, ("key_codes", "key_scales"))
-    _cache4(value_codes, value_scales, dev, ("value_codes", "value_scales"), shape)
+    args, dev, (T, Hk, D), begin, end = _append(key, value, positions, inv_freq, key_gscale, value_gscale,
+                                                ("key_gscale", "value_gscale"), slot_mapping, k_weight, eps, weight_offset,
+                                                interleaved, 8 if interleaved else 16, torch)
+    shape = _cache4(key_codes, key_scales, dev, ("key_codes", "key_scales"), torch)
+    _cache4(value_codes, value_scales, dev, ("value_codes", "value_scales"), torch, shape)
     B, heads, bs, dim = shape
     if heads != Hk or dim != D:
         raise ValueError(f"the cache holds {heads} heads of {dim}, keys have {Hk} of {D}")
-    at = [t.data_ptr() for t in (key_codes, key_scales, value_codes, value_scales)]
-    rows = B * Hk * bs
-    _refuse_ranges([(name, p, p + rows * n) for name, p, n in zip(
-        ("key_codes", "key_scales", "value_codes", "value_scales"), at, (D // 2, D // 16, D // 2, D // 16))], ins)
+    at = key_codes.data_ptr(), key_scales.data_ptr(), value_codes.data_ptr(), value_scales.data_ptr()
+    n = B * Hk * bs * (D // 16)
+    # ranges are disjoint if and only if, both in rising order, each ends before the next begins
+    starts, ends = sorted((*at, *begin)), sorted((at[0] + 8 * n, at[1] + n, at[2] + 8 * n, at[3] + n, *end))
+    if any(map(operator.gt, ends, starts[1:])):
+        _refuse_ranges([(name, p, p + m) for name, p, m in zip(
+            ("key_codes", "key_scales", "value_codes", "value_scales"), at, (8 * n, n, 8 * n, n))],
+            [("key, value or slot_mapping", i, e) for i, e in zip(begin, end)])
     _call(dev, lib.nvfp4_kv_fp4_append, *args, *at, B, bs)
 
 
@@ -357,7 +370,7 @@ def nvfp4_kv_fp4_load(codes, scales, gscale, slot_mapping=None, out_dtype=None, 
     torch = _base._torch()
     lib = _lib()
     dev = _cuda(codes, "codes")
-    B, Hk, bs, D = _cache4(codes, scales, dev, ("codes", "scales"))
+    B, Hk, bs, D = _cache4(codes, scales, dev, ("codes", "scales"), torch)
     if gscale.dtype != torch.float32 or gscale.numel() != 1 or gscale.device != dev:
         raise ValueError(f"gscale must be one float32 value on {dev}")
     T = B * bs
@@ -379,11 +392,10 @@ def nvfp4_kv_fp4_load(codes, scales, gscale, slot_mapping=None, out_dtype=None, 
             raise ValueError(f"out must be contiguous [{T}, {Hk}, {D}], got {list(out.shape)}")
         if out.device != dev:
             raise ValueError(f"out must live on {dev}, got {out.device}")
-        o, c, s = out.data_ptr(), codes.data_ptr(), scales.data_ptr()
-        rows = B * Hk * bs
-        _refuse_ranges([("out", o, o + out.numel() * out.element_size())],
-                       [("codes", c, c + rows * D // 2), ("scales", s, s + rows * D // 16),
-                        ("slot_mapping", sm or 0, (sm or 0) + (8 * T if sm else 0))])
+        o, c, s, n, m = out.data_ptr(), codes.data_ptr(), scales.data_ptr(), B * Hk * bs * (D // 16), sm or 0
+        end = o + T * Hk * D * (4 if out.dtype is torch.float32 else 2)
+        if o < c + 8 * n and c < end or o < s + n and s < end or o < m + 8 * T and m < end:
+            _refuse_ranges([("out", o, end)], [("codes", c, c + 8 * n), ("scales", s, s + n), ("slot_mapping", m, m + 8 * T if m else 0)])
     _call(dev, lib.nvfp4_kv_fp4_load, codes.data_ptr(), scales.data_ptr(), B, Hk, bs, D, gscale.data_ptr(), sm, T,
           out.data_ptr(), _base._dtype_code(out.dtype))
     return out
@@ -398,24 +410,24 @@ def _workspace_bytes(*sizes):
     return _lib().nvfp4_kv_fp4_attention_workspace(*sizes)
 
 
-def _attention(fn_name, q, key_codes, key_scales, value_codes, value_scales, key_gscale, value_gscale, block_table,
+def _attention(fn, q, key_codes, key_scales, value_codes, value_scales, key_gscale, value_gscale, block_table,
                query_start, seq_lens, scale, softcap, slopes, extra, max_query_len, max_seq_len, out):
     torch = _base._torch()
-    lib = _lib()
     dev = _cuda(q, "q")
     if q.dim() != 3:
         raise ValueError("q must be 3-D [tokens, heads, head_dim]")
-    if q.dtype != torch.bfloat16 and q.dtype != torch.float16:
-        raise ValueError(f"q must be bfloat16 or float16, got {q.dtype}")
+    dtype = q.dtype
+    if dtype != torch.bfloat16 and dtype != torch.float16:
+        raise ValueError(f"q must be bfloat16 or float16, got {dtype}")
     T, H, D = q.shape
-    shape = _cache4(key_codes, key_scales, dev, ("key_codes", "key_scales"))
-    _cache4(value_codes, value_scales, dev, ("value_codes", "value_scales"), shape)
+    shape = _cache4(key_codes, key_scales, dev, ("key_codes", "key_scales"), torch)
+    _cache4(value_codes, value_scales, dev, ("value_codes", "value_scales"), torch, shape)
     B, Hk, bs, dim = shape
     if dim != D:
         raise ValueError(f"the cache holds heads of {dim}, q has {D}")
     if H < 1 or H > 1024 or H % Hk:
         raise ValueError(f"{H} heads (1 to 1024) must be a multiple of {Hk} KV heads")
-    q_ts, q_hs = _rows(q, (T, H, D), q.dtype, dev, "q")
+    q_ts, q_hs = _strides(q, q.shape, dtype, dev, "q")
     for s, name in ((key_gscale, "key_gscale"), (value_gscale, "value_gscale")):
         if s.dtype != torch.float32 or s.numel() != 1 or s.device != dev:
             raise ValueError(f"{name} must be one float32 value on {dev}")
@@ -441,12 +453,21 @@ def _attention(fn_name, q, key_codes, key_scales, value_codes, value_scales, key
     need = _workspace_bytes(T, H, Hk, D, R, max_query_len, max_seq_len)
     # from the caching allocator on the current stream: no two calls that may run at once share one
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _call(dev, getattr(lib, fn_name), q.data_ptr(), _base.NVFP4_BF16 if q.dtype == torch.bfloat16 else _base.NVFP4_F16,
+    _call(dev, fn, q.data_ptr(), _base.NVFP4_BF16 if dtype is torch.bfloat16 else _base.NVFP4_F16,
           T, H, Hk, D, q_ts, q_hs, key_codes.data_ptr(), key_scales.data_ptr(), value_codes.data_ptr(),
           value_scales.data_ptr(), key_gscale.data_ptr(), value_gscale.data_ptr(), B, bs, block_table.data_ptr(), R, W,
-          table_ld, qs, sl, D ** -0.5 if scale is None else float(scale), float(softcap), sp, *extra(T, R, dev),
+          table_ld, qs, sl, D ** -0.5 if scale is None else scale, softcap, sp, *extra(T, R, dev),
           max_query_len, max_seq_len, out.data_ptr(), out_ts, out_hs, None if ws is None else ws.data_ptr(), need)
     return out
+
+
+def _document_arguments(doc_start, prefix_lens, T, R, dev):
+    """Arguments of the documents' and the prefixes' masks."""
+    if doc_start is None and prefix_lens is None:
+        return None, None
+    i32 = _base._torch().int32
+    return (None if doc_start is None else _vector(doc_start, T, i32, dev, "doc_start"),
+            None if prefix_lens is None else _vector(prefix_lens, R, i32, dev, "prefix_lens"))
 
 
 def nvfp4_kv_fp4_attention(q, key_codes, key_scales, value_codes, value_scales, key_gscale, value_gscale, block_table,
@@ -455,15 +476,9 @@ def nvfp4_kv_fp4_attention(q, key_codes, key_scales, value_codes, value_scales, 
     """:func:`nvfp4_kv_fp8_attention` over the 4-bit cache that :func:`nvfp4_kv_fp4_append` fills: the same definition,
     masks and arguments, but for the cache, whose shape gives ``block_size`` and the number of KV heads, and its scales
     (encode direction, as given to the append)."""
-    torch = _base._torch()
-
-    def extra(T, R, dev):
-        return (None if doc_start is None else _vector(doc_start, T, torch.int32, dev, "doc_start"),
-                None if prefix_lens is None else _vector(prefix_lens, R, torch.int32, dev, "prefix_lens"))
-
-    return _attention("nvfp4_kv_fp4_attention", q, key_codes, key_scales, value_codes, value_scales, key_gscale,
-                      value_gscale, block_table, query_start, seq_lens, scale, softcap, slopes, extra, max_query_len,
-                      max_seq_len, out)
+    return _attention(_lib().nvfp4_kv_fp4_attention, q, key_codes, key_scales, value_codes, value_scales, key_gscale,
+                      value_gscale, block_table, query_start, seq_lens, scale, softcap, slopes,
+                      functools.partial(_document_arguments, doc_start, prefix_lens), max_query_len, max_seq_len, out)
 
 
 def nvfp4_kv_fp4_tree_attention(q, key_codes, key_scales, value_codes, value_scales, key_gscale, value_gscale,
@@ -471,7 +486,7 @@ def nvfp4_kv_fp4_tree_attention(q, key_codes, key_scales, value_codes, value_sca
                                 positions=None, max_query_len=None, max_seq_len=None, out=None):
     """:func:`nvfp4_kv_fp8_tree_attention` over the 4-bit cache; the cache's arguments as
     :func:`nvfp4_kv_fp4_attention`."""
-    return _attention("nvfp4_kv_fp4_tree_attention", q, key_codes, key_scales, value_codes, value_scales, key_gscale,
+    return _attention(_lib().nvfp4_kv_fp4_tree_attention, q, key_codes, key_scales, value_codes, value_scales, key_gscale,
                       value_gscale, block_table, query_start, seq_lens, scale, softcap, slopes,
                       functools.partial(_tree_arguments, tree_mask, positions), max_query_len, max_seq_len, out)
 
@@ -536,13 +551,12 @@ def nvfp4_verify_drafted(target_probs, draft_probs, tokens, query_start, accept_
     to = _vector(out, rows, i32, dev, "out")
     tp = target_probs.data_ptr()
     dp = None if draft_probs is None else draft_probs.data_ptr()
-    ins = [("tokens", tk, tk + 4 * rows), ("query_start", qs, qs + 4 * R + 4), ("accept_u", au, au + 4 * rows),
-           ("sample_u", su, su + 4 * R)]
-    if rows:
-        ins.append(("target_probs", tp, tp + 4 * ((rows - 1) * ld + V)))
-        if dp is not None:
-            ins.append(("draft_probs", dp, dp + 4 * ((rows - 1) * dld + V)))
-    _refuse_ranges([("accepted", ac, ac + 4 * R), ("out", to, to + 4 * rows)], ins)
+    wide, far = (4 * ((rows - 1) * x + V) if rows else 0 for x in (ld, dld))
+    begin, end = (tk, qs, au, su, tp, dp or 0), (tk + 4 * rows, qs + 4 * R + 4, au + 4 * rows, su + 4 * R, tp + wide, dp + far if dp else 0)
+    starts, ends = sorted((ac, to, *begin)), sorted((ac + 4 * R, to + 4 * rows, *end))
+    if any(map(operator.gt, ends, starts[1:])):
+        _refuse_ranges([("accepted", ac, ac + 4 * R), ("out", to, to + 4 * rows)],
+                       zip(("tokens", "query_start", "accept_u", "sample_u", "target_probs", "draft_probs"), begin, end))
     need = lib.nvfp4_verify_drafted_workspace(R, V)
     # from the caching allocator on the current stream: no two calls that may run at once share one
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None

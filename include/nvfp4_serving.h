@@ -52,7 +52,7 @@ extern "C" {
  * that holds them.
  *
  *   q, k          device, [tokens, q_heads, head_dim] and [tokens, k_heads, head_dim] of dtype (F32, BF16 or
- *                 F16), token and head strides in elements (strides in bytes multiples of 16, head_dim
+ *                 F16), token and head strides in elements (in bytes multiples of 16 and below 2^32, head_dim
  *                 contiguous); 16-byte aligned.  k may be absent: k_heads 0.
  *   head_dim      a multiple of 16, 16 .. NVFP4_MAX_HEAD_DIM; q_heads 1 .. 1024; k_heads 0 .. 1024.
  *   positions     device, int32[tokens]; inv_freq: device, float[num_freq].  Both NULL with num_freq 0: no

@@ -325,10 +325,15 @@ def test_fp4_load_of_every_byte():
     scales = np.zeros((256, 1, 2, 4), np.uint8)
     codes[:] = np.arange(64, dtype=np.uint8).reshape(1, 1, 2, 32) * 4 + np.arange(256, dtype=np.uint8).reshape(256, 1, 1, 1) % 4
     scales[:] = np.arange(256, dtype=np.uint8).reshape(256, 1, 1, 1)
-    g = np.float32(3.0)
-    got = nv.nvfp4_kv_fp4_load(torch.from_numpy(codes).to(DEV), torch.from_numpy(scales).to(DEV), torch.tensor([g], device=DEV))
-    want = (osv.decode4(codes, scales).astype(np.float32) / g).transpose(0, 2, 1, 3).reshape(512, 1, 64)
-    assert np.array_equal(got.cpu().numpy(), want)
+    up = [torch.from_numpy(x).to(DEV) for x in (codes, scales)]
+    rng = np.random.default_rng(0)
+    exact = osv.decode4(codes, scales).astype(np.float32).transpose(0, 2, 1, 3).reshape(512, 1, 64)
+    for g in [3.0, 1.0, 56.0, np.nextafter(np.float32(2), np.float32(1)), 2.0 ** -100, 2.0 ** 100, 1e-36, 2.0 ** 126, *np.exp2(rng.uniform(-90, 90, 40))]:
+        g = np.float32(g)
+        with np.errstate(over="ignore", under="ignore"):
+            want = exact / g
+        got = nv.nvfp4_kv_fp4_load(*up, torch.tensor([g], device=DEV)).cpu().numpy()
+        assert np.array_equal(got.view(np.int32), want.view(np.int32)), g
 
 
 def test_append_from_a_fused_row_without_slots_and_empty():

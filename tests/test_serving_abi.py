@@ -66,7 +66,7 @@ def test_rope_validation():
                dict(off=NAN), dict(off=INF)):
         assert _rope(**kw) == EINVAL, kw
     for kw in (dict(T=-1), dict(T=1 << 31), dict(H=0), dict(H=1025), dict(Hk=-1), dict(Hk=1025), dict(D=0), dict(D=24),
-               dict(D=528), dict(n=-8), dict(n=12), dict(n=72), dict(qts=-512), dict(khs=-128), dict(qts=1 << 41),
+               dict(D=528), dict(n=-8), dict(n=12), dict(n=72), dict(qts=-512), dict(khs=-128), dict(qts=1 << 41), dict(qts=1 << 31), dict(kohs=1 << 31),
                dict(qots=256), dict(qohs=64), dict(kots=0), dict(kohs=0)):
         assert _rope(**kw) == ESHAPE, kw
     for kw in (dict(q=P + 8), dict(k=P + 8), dict(qo=P + 8), dict(ko=P + 8), dict(qts=516), dict(khs=132, kts=512),
@@ -380,14 +380,14 @@ STUBS = '''
 namespace nvfp4 {
 // what the kernels take for granted
 hipError_t launch_heads(HeadArgs a, nvfp4_dtype, HeadSink sink, hipStream_t) {
-  const bool ok = a.tokens >= 1 && a.head_dim % 16 == 0 && a.num_freq % 8 == 0 && 2 * a.num_freq <= a.head_dim && a.group[0].heads >= 1 &&
-                  a.group[0].heads + a.group[1].heads <= 2048 && (a.num_freq == 0 || (a.positions && a.inv_freq)) &&
+  const bool ok = a.tokens >= 1 && a.head_dim % 16 == 0 && a.num_freq % 8 == 0 && 2 * a.num_freq <= a.head_dim && a.group[0].heads.d >= 1 &&
+                  a.group[0].heads.d + a.group[1].heads.d <= 2048 && (a.num_freq == 0 || (a.positions && a.inv_freq)) &&
                   (sink == HeadSink::Same ? a.group[0].out != nullptr : a.group[0].cache && a.group[1].cache && a.num_slots > 0) &&
-                  (sink != HeadSink::Fp4 || (a.num_slots * a.group[0].heads < (1ll << 31) && (a.interleaved || a.num_freq % 16 == 0)));
+                  (sink != HeadSink::Fp4 || (a.num_slots * a.group[0].heads.d < (1ll << 31) && (a.interleaved || a.num_freq % 16 == 0)));
   return ok ? hipSuccess : hipErrorInvalidValue;
 }
-hipError_t launch_fp4_load(const Fp4LoadArgs& a, bool, int64_t tokens, hipStream_t) {
-  return tokens > 0 && a.num_slots * a.kv_heads < (1ll << 31) ? hipSuccess : hipErrorInvalidValue;
+hipError_t launch_fp4_load(Fp4LoadArgs a, bool, hipStream_t) {
+  return a.tokens > 0 && a.head_bits >= 6 && a.head_bits <= 8 && a.num_slots * a.kv_heads < (1ll << 31) ? hipSuccess : hipErrorInvalidValue;
 }
 hipError_t launch_verify(const VerifyArgs& a, hipStream_t) {
   return a.requests > 0 && a.requests <= 8192 && (int64_t)a.chunks * kVerifyChunk < (1ll << 31) && a.sums ? hipSuccess : hipErrorInvalidValue;
