@@ -77,39 +77,34 @@ __device__ __forceinline__ double sum_all(double x, double* lds) {
   return s;
 }
 
-// Inclusive sum over the threads up to this one, and over all.
-__device__ __forceinline__ double scan_all(double x, double* lds, double& all) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// Inclusive sum over a wavefront's lanes up to this one.
+__device__ __forceinline__ double scan_wave(double x) {
+  const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const double up = __shfl_up(x, d);
     if (lane >= d) x += up;
   }
-  if (lane == 63) lds[wave] = x;
-  __syncthreads();
-  double before = 0.0;
-  all = 0.0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    if (w == wave) before = all;
-    all += lds[w];
-  }
-  __syncthreads();
-  return before + x;
+  return x;
 }
 
-// Lowest (LEAST) or highest of the workgroup's numbers.
-template <bool LEAST>
-__device__ __forceinline__ int32_t extreme(int32_t x, int32_t* lds) {
+// kEach numbers of a row from v on: whole where `all`, else those below the vocabulary's end.
+struct __attribute__((packed, aligned(4))) Four {
+  float x[4];
+};
+
+__device__ __forceinline__ void load_row(const float* row, int32_t v, int32_t vocab, float (&x)[kEach]) {
+  if (v + kEach <= vocab) {
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) x = LEAST ? min(x, __shfl_xor(x, d)) : max(x, __shfl_xor(x, d));
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
-  __syncthreads();
-  int32_t s = lds[0];
+    for (int i = 0; i < kEach; i += 4) {
+      const Four f = *reinterpret_cast<const Four*>(row + v + i);
 #pragma unroll
-  for (int w = 1; w < kWaves; ++w) s = LEAST ? min(s, lds[w]) : max(s, lds[w]);
-  __syncthreads();
-  return s;
+      for (int k = 0; k < 4; ++k) x[i + k] = f.x[k];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) x[i] = v + i < vocab ? row[v + i] : 0.0f;
+  }
 }
 
 // grid: x over chunks of the vocabulary, y over requests.
@@ -147,59 +142,72 @@ __global__ void __launch_bounds__(kThreads) verify_sum_kernel(VerifyArgs a) {
   }
 }
 
+// A workgroup a request.  Every wavefront finds the chunk by itself (64 chunks a look), with no barrier.
 __global__ void __launch_bounds__(kThreads) verify_pick_kernel(VerifyArgs a) {
-  __shared__ double lds[kWaves];
-  __shared__ int32_t ints[kWaves];
-  __shared__ double carry;
+  __shared__ double totals[kWaves];
+  __shared__ int32_t firsts[kWaves], ends[kWaves];
   constexpr int32_t kNone = 0x7FFFFFFF;
   const int32_t r = blockIdx.x;
   const Rows q = rows_of(a, r);
   if (q.last < q.start) return;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int32_t row = q.start + a.accepted[r];
-  Weights w = weights_of(a, q, row);
+  const double u = a.sample_u[r];
   const double* sums = a.sums + (int64_t)r * a.chunks * 2;
   // the row's sum, of the weights or, where they are all zero, of the target's probabilities
   double left = 0.0, whole = 0.0;
-  for (int32_t b = 0; b < a.chunks; b += kThreads) {
-    const int32_t c = b + tid;
-    double l, p;
-    scan_all(c < a.chunks ? sums[2 * c] : 0.0, lds, l);
-    scan_all(c < a.chunks ? sums[2 * c + 1] : 0.0, lds, p);
+  for (int32_t b = 0; b < a.chunks; b += 64) {
+    const int32_t c = b + lane;
+    double l = c < a.chunks ? sums[2 * c] : 0.0, p = c < a.chunks ? sums[2 * c + 1] : 0.0;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      l += __shfl_xor(l, d);
+      p += __shfl_xor(p, d);
+    }
     left += l;
     whole += p;
   }
   const bool plain = !(left > 0.0);
+  Weights w = weights_of(a, q, row);
   if (plain) w = Weights{w.p, nullptr, -1};
-  const double aim = (double)a.sample_u[r] * (plain ? whole : left);
+  const double aim = u * (plain ? whole : left);
   // the first chunk whose sum passes the aim, or the last that has any weight
-  int32_t chosen = kNone, last = -1;
+  int32_t chosen = -1, last = -1;
   double before = 0.0, base = 0.0;
-  for (int32_t b = 0; b < a.chunks && chosen == kNone; b += kThreads) {
-    const int32_t c = b + tid;
+  for (int32_t b = 0; b < a.chunks && chosen < 0; b += 64) {
+    const int32_t c = b + lane;
     const double x = c < a.chunks ? sums[2 * c + (plain ? 1 : 0)] : 0.0;
-    double all;
-    const double upto = before + scan_all(x, lds, all);
-    last = max(last, extreme<false>(x > 0.0 ? c : -1, ints));
-    chosen = extreme<true>(x > 0.0 && upto > aim ? c : kNone, ints);
-    if (c == chosen) carry = upto - x;
-    before += all;
+    const double sum = scan_wave(x), upto = before + sum;
+    const uint64_t some = __ballot(x > 0.0), passed = __ballot(x > 0.0 && upto > aim);
+    if (some) last = b + 63 - __builtin_clzll(some);
+    if (passed) {
+      const int at = __builtin_ctzll(passed);
+      chosen = b + at;
+      base = __shfl(upto - x, at);
+    }
+    before = __shfl(upto, 63);
   }
-  __syncthreads();
-  if (chosen != kNone) base = carry;
-  const bool at_end = chosen == kNone;
+  const bool at_end = chosen < 0;
   if (at_end) chosen = last;
   int32_t token = -1;
   if (chosen >= 0) {
     const int32_t v0 = chosen * kVerifyChunk + tid * kEach;
-    double x[kEach], sum = 0.0, all;
+    float p[kEach], d[kEach];
+    load_row(w.p, v0, a.vocab, p);
+    if (w.q) load_row(w.q, v0, a.vocab, d);
+    double x[kEach], sum = 0.0;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      const int32_t v = v0 + i;
-      x[i] = v < a.vocab ? weight_at(w, v, w.p[v], w.q ? w.q[v] : 0.0f) : 0.0;
+      x[i] = weight_at(w, v0 + i, p[i], w.q ? d[i] : 0.0f);
       sum += x[i];
     }
-    double upto = base + (scan_all(sum, lds, all) - sum);
+    const double mine = scan_wave(sum);
+    if (lane == 63) totals[wave] = mine;
+    __syncthreads();
+    double upto = base;
+#pragma unroll
+    for (int k = 0; k < kWaves; ++k) upto += k < wave ? totals[k] : 0.0;
+    upto += mine - sum;
     int32_t first = kNone, end = -1;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
@@ -209,10 +217,22 @@ __global__ void __launch_bounds__(kThreads) verify_pick_kernel(VerifyArgs a) {
         if (first == kNone && upto > aim) first = v0 + i;
       }
     }
+    // the lowest of the lanes' first, the highest of their ends: lanes hold rising parts of the chunk
+    const uint64_t found = __ballot(first != kNone), some = __ballot(end >= 0);
+    const int32_t f = found ? __shfl(first, __builtin_ctzll(found)) : kNone, e = some ? __shfl(end, 63 - __builtin_clzll(some)) : -1;
+    if (lane == 0) {
+      firsts[wave] = f;
+      ends[wave] = e;
+    }
+    __syncthreads();
+    int32_t at = kNone, tail = -1;
+#pragma unroll
+    for (int k = 0; k < kWaves; ++k) {
+      at = min(at, firsts[k]);
+      tail = max(tail, ends[k]);
+    }
     // (where rounding leaves the chunk's sum at the aim: its last token with a weight)
-    first = extreme<true>(at_end ? kNone : first, ints);
-    end = extreme<false>(end, ints);
-    token = first == kNone ? end : first;
+    token = at_end || at == kNone ? tail : at;
   }
   for (int32_t t = q.start + tid; t <= q.last; t += kThreads) a.out[t] = t < row ? a.tokens[t + 1] : t == row ? token : -1;
 }
