@@ -9,9 +9,9 @@ namespace {
 constexpr int64_t kMaxTiles = 4096;  // bound of a grid dimension
 constexpr int64_t kShort = 8 * kStreamUnit;  // positions that a workgroup walks over alone
 
-// `groups`: workgroups that share a compute unit in the streaming kernel.
+// `groups`: workgroups that share a compute unit in the streaming kernel; `most`: rows that it can take at once.
 AttnPlan plan(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t requests,
-              int64_t max_query_len, int64_t max_seq_len, int (*groups)(int, int)) {
+              int64_t max_query_len, int64_t max_seq_len, int (*groups)(int, int), int64_t most) {
   AttnPlan p{};
   const int64_t group = heads / kv_heads, rows = max_query_len * group;
   // Short sequences: one launch of a workgroup per item and no join (one token over 500 and 1000 positions,
@@ -31,6 +31,15 @@ AttnPlan plan(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
     // 128 and 256 dims (all 6001 long) 938 and 407, 854 and 412.
     p.kernel = AttnKernel::Stream32;
     p.rows = 32;
+    // Over the 4-bit cache decoding is most of a tile's work, and tiles of 48 rows where they are fewer than those of 32
+    // pay from some thousand positions on: below, a workgroup takes few steps and each is longer.  Trees of 12 tokens
+    // with 4 heads each over 1500, 6001 and 24000 positions (32 against 48 rows): 16 requests of 128 dims 33 and 37, 54 and
+    // 52, 149 and 121 us; 64 of them 57 and 72, 181 and 139, 662 and 427; 16 of 64 dims 29 and 32, 46 and 43, 108 and 94.
+    // Of 24 tokens (three tiles or two), 128 dims: 42 and 45, 78 and 76, 224 and 201.
+    if (most == 48 && max_seq_len >= 4096 && rows <= 96 && (rows + 47) / 48 < (rows + 31) / 32) {
+      p.kernel = AttnKernel::Stream48;
+      p.rows = 48;
+    }
   } else {
     p.kernel = AttnKernel::Tiled;
     p.rows = 256;
@@ -71,12 +80,13 @@ AttnPlan plan(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
 
 AttnPlan plan_attention(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
                         int64_t requests, int64_t max_query_len, int64_t max_seq_len) {
-  return plan(tokens, heads, kv_heads, head_dim, requests, max_query_len, max_seq_len, stream_groups);
+  return plan(tokens, heads, kv_heads, head_dim, requests, max_query_len, max_seq_len, stream_groups, 32);
 }
 
 AttnPlan plan_attention_fp4(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t requests,
                             int64_t max_query_len, int64_t max_seq_len) {
-  return plan(tokens, heads, kv_heads, head_dim, requests, max_query_len, max_seq_len, stream_groups_fp4);
+  return plan(tokens, heads, kv_heads, head_dim, requests, max_query_len, max_seq_len, stream_groups_fp4,
+              head_dim <= 128 ? 48 : 32);
 }
 
 }  // namespace nvfp4

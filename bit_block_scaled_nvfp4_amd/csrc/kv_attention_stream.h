@@ -30,7 +30,13 @@
 // Over the 4-bit cache (NVFP4) the products are the same; what differs is how their operands are formed.
 // Keys: a lane holds a quarter of a key's dims, contiguous (head_dim / 8 bytes and head_dim / 64 scale bytes), and a
 // step of 32 dims takes 8 of each of the four lanes.  Values: codes of two keys are put together nibble by nibble, so
-// that one conversion gives a dim's two keys side by side and one packed product gives both their scales.
+// that one conversion gives a dim's two keys side by side and one packed product gives both their scales.  The codes take half
+// the registers, so that two workgroups of 256 dims share a compute unit, and up to 128 dims a tile may have 48 rows.
+// Measured: 64 requests x up to 8000 positions, one token each, 24 heads over 4 of 256 dims, 321 MB: 74 us and 5 for the
+// join, 4.3 TB/s; half of its time is vector instructions (70 a product of 16 x 16 x 32 at 16 rows), the rest waits.  Forming
+// the rows' addresses by scalar instructions where blocks hold a multiple of 16 positions took 75 us, and requesting keys
+// without a condition (so that the wait for values is not one for them too) 76; 16 trees of 12 tokens with 4 heads each over
+// 6001 positions of 128 dims 44 us with both, 45 without: left out.
 #pragma once
 
 #include "kv_attention_common.h"
@@ -182,10 +188,15 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 x, u32x4 y, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
 }
 
+// 48 rows, and 32 rows of three workgroups a compute unit, leave no registers for their queries, which are the same in
+// all wavefronts.
+template <Cache C, int D, int NQ>
+constexpr bool kQueriesInLds = C == Cache::Fp4 && (NQ == 3 || (D == 64 && NQ == 2));
+
 // State of a wavefront over one segment: NQ column tiles of 16 query rows.
-template <int D, int NQ>
+template <Cache C, int D, int NQ>
 struct State {
-  u32x4 q[NQ][D / 32];
+  u32x4 q[kQueriesInLds<C, D, NQ> ? 1 : NQ][D / 32];  // the rows' operands, where registers hold them
   f32x4 acc[NQ][D / 16];  // acc[.][t][i]: dim (4 g + i) * (D / 16) + t
   float m[NQ], l[NQ];     // l: this lane's keys only
   int32_t lo[NQ], hi[NQ];  // of the lane's rows, as in Row; their numbers are formed again where needed
@@ -196,7 +207,7 @@ struct State {
 
 template <Cache C, int D, bool BF16, int NQ, Scores SCORES>
 __device__ __forceinline__ void step(const Segment& sg, const Request& rq, const Keys<C, D>& kc, Values<C, D>& vc, int32_t slot,
-                                     int32_t j0, float c, float cap, int lane, State<D, NQ>& s) {
+                                     int32_t j0, float c, float cap, int lane, const u32x4* queries, State<C, D, NQ>& s) {
   const int g = lane >> 4;
   f32x4 x[2][NQ];
 #pragma unroll
@@ -206,7 +217,10 @@ __device__ __forceinline__ void step(const Segment& sg, const Request& rq, const
 #pragma unroll
   for (int j = 0; j < D / 64; ++j)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
+      u32x4 q[NQ];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) q[n] = kQueriesInLds<C, D, NQ> ? queries[(n * (D / 32) + 2 * j + h) * 64 + lane] : s.q[kQueriesInLds<C, D, NQ> ? 0 : n][2 * j + h];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         u32x4 k;
@@ -218,10 +232,11 @@ __device__ __forceinline__ void step(const Segment& sg, const Request& rq, const
           k = u32x4{lo.x, lo.y, hi.x, hi.y};
         }
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) x[t][n] = mfma16<BF16>(k, s.q[n][2 * j + h], x[t][n]);
+        for (int n = 0; n < NQ; ++n) x[t][n] = mfma16<BF16>(k, q[n], x[t][n]);
         // decode a few operands at a time: all of them at once take twice the registers of their codes
         if (t == 1) __builtin_amdgcn_sched_barrier(0);
       }
+    }
 
   __builtin_amdgcn_sched_barrier(0);  // the phases' instructions stay apart, to keep their registers few
   // wave-uniform: every position of the step is in the cache and seen by every row of the tile
@@ -410,14 +425,14 @@ __device__ __forceinline__ void step(const Segment& sg, const Request& rq, const
 }
 
 template <Cache C, int D, bool BF16, int NQ, Scores SCORES>
-__device__ __forceinline__ void segment(const Segment& sg, bool split, int32_t worker, float* lds) {
+__device__ __forceinline__ void segment(const Segment& sg, bool split, int32_t worker, float* lds, u32x4* queries) {
   const AttnArgs& a = args();
   constexpr int kRows = 16 * NQ;
   constexpr int kPitch = D + 4;  // floats; 16 bytes a row apart, so a store's 8 lanes differ in banks
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int g = lane >> 4, d16 = lane & 15;
   const Request rq = request_of(a, sg.r);
-  State<D, NQ> s;
+  State<C, D, NQ> s;
   const float c = a.scale * scale_of<C>(a.ks) * kLog2e, cap = SCORES != Scores::Plain ? a.cap : 0.0f;
 
   int32_t lo_min = 0x7FFFFFFF, hi_max = 0, lo_max = 0, hi_min = 0x7FFFFFFF;
@@ -435,8 +450,12 @@ __device__ __forceinline__ void segment(const Segment& sg, bool split, int32_t w
     // the dims of step j that this lane's codes hold
     const uint16_t* qp = a.q + (int64_t)w.token * a.q_ts + (int64_t)w.head * a.q_hs + g * (C == Cache::Fp4 ? D / 4 : 16);
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j)
-      s.q[n][j] = w.token >= 0 ? *reinterpret_cast<const u32x4*>(qp + (C == Cache::Fp4 ? 8 * j : 64 * (j >> 1) + 8 * (j & 1))) : u32x4{0, 0, 0, 0};
+    for (int j = 0; j < D / 32; ++j) {
+      if (kQueriesInLds<C, D, NQ> && (n * (D / 32) + j) % kWaves != wave) continue;
+      const u32x4 q = w.token >= 0 ? *reinterpret_cast<const u32x4*>(qp + (C == Cache::Fp4 ? 8 * j : 64 * (j >> 1) + 8 * (j & 1))) : u32x4{0, 0, 0, 0};
+      if constexpr (kQueriesInLds<C, D, NQ>) queries[(n * (D / 32) + j) * 64 + lane] = q;
+      else s.q[n][j] = q;
+    }
     if (w.token >= 0) {
       // a tree's rows see at most the request's keys, and below ctx all of them
       lo_min = min(lo_min, w.lo);
@@ -452,6 +471,7 @@ __device__ __forceinline__ void segment(const Segment& sg, bool split, int32_t w
     lo_max = max(lo_max, __shfl_xor(lo_max, d));
     hi_min = min(hi_min, __shfl_xor(hi_min, d));
   }
+  if constexpr (kQueriesInLds<C, D, NQ>) __syncthreads();
   s.lo_all = __builtin_amdgcn_readfirstlane(lo_max);
   s.hi_all = __builtin_amdgcn_readfirstlane(hi_min);
   lo_min = __builtin_amdgcn_readfirstlane(lo_min);
@@ -495,14 +515,14 @@ __device__ __forceinline__ void segment(const Segment& sg, bool split, int32_t w
       __builtin_amdgcn_sched_barrier(0);
       load_values<D, NQ == 1>(a, s0, vbase, ln, v);
       if (u > u0) load_keys<D, NQ == 1>(a, s1, kbase, ln, k1);
-      step<C, D, BF16, NQ, SCORES>(sg, rq, k0, v, s0, u * kUnit + wave * kStep, c, cap, ln, s);
+      step<C, D, BF16, NQ, SCORES>(sg, rq, k0, v, s0, u * kUnit + wave * kStep, c, cap, ln, queries, s);
       if (u - 1 < u0) break;
       s0 = slots(e2, u - 2);
       e1 = entries(u - 3);
       __builtin_amdgcn_sched_barrier(0);
       load_values<D, NQ == 1>(a, s1, vbase, ln, v);
       if (u - 1 > u0) load_keys<D, NQ == 1>(a, s0, kbase, ln, k0);
-      step<C, D, BF16, NQ, SCORES>(sg, rq, k1, v, s1, (u - 1) * kUnit + wave * kStep, c, cap, ln, s);
+      step<C, D, BF16, NQ, SCORES>(sg, rq, k1, v, s1, (u - 1) * kUnit + wave * kStep, c, cap, ln, queries, s);
       if (u - 2 < u0) break;
     }
   }
@@ -579,6 +599,7 @@ template <Cache C, int D, bool BF16, int NQ, Scores SCORES>
 __global__ void __launch_bounds__(kThreads, C == Cache::Fp4 ? stream_groups_fp4(D, 16 * NQ) : stream_groups(D, 16 * NQ)) attention_stream_kernel(AttnArgs) {
   constexpr int kRows = 16 * NQ;
   __shared__ __align__(16) float lds[kWaves * 16 * (D + 4) + kWaves * kRows * 2];
+  __shared__ u32x4 queries[kQueriesInLds<C, D, NQ> ? NQ * (D / 32) * 64 : 1];
   __shared__ Share<kThreads> share;
   Segment s;
   if (args().workers == 0) {
@@ -591,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, C == Cache::Fp4 ? stream_groups_fp4(
     s.u0 = 0;
     s.u1 = (int32_t)(((uint32_t)q.keys + kUnit - 1) / kUnit);
     const int32_t tiles = (int32_t)(((uint32_t)q.count * a.group.d + kRows - 1) / kRows);
-    for (s.tile = blockIdx.z; s.tile < tiles; s.tile += gridDim.z) segment<C, D, BF16, NQ, SCORES>(s, false, 0, lds);
+    for (s.tile = blockIdx.z; s.tile < tiles; s.tile += gridDim.z) segment<C, D, BF16, NQ, SCORES>(s, false, 0, lds, queries);
     return;
   }
   share.begin(kRows, kUnit);
@@ -599,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, C == Cache::Fp4 ? stream_groups_fp4(
   if (threadIdx.x == 0) header->last_worker = -1;
   while (share.next(kRows, kUnit, s)) {
     if (s.first && !s.last && threadIdx.x == 0) *header = Header{s.r, s.tile, s.kv_head, s.last_worker, share.worker, {0, 0, 0}};
-    segment<C, D, BF16, NQ, SCORES>(s, true, uniform(share.worker), lds);
+    segment<C, D, BF16, NQ, SCORES>(s, true, uniform(share.worker), lds, queries);
   }
 }
 
@@ -638,36 +659,108 @@ __device__ __forceinline__ void join_pieces(const AttnArgs& a, const Header& h, 
   }
 }
 
-// Joins the pieces of the items that were shared out: blocks (b, y) take rows of the item that begins in
-// workgroup b's share and ends in that of worker last_worker.  With few pieces a wavefront takes a whole
-// row and a block four; with more (one long request over all workers) a block takes one row and its
-// wavefronts a quarter of the pieces each.
+// One row of the output: its sums over (1 / vs times) the sum of its weights.
 template <Cache C, int D, bool BF16>
-__global__ void __launch_bounds__(kThreads) attention_join_kernel(AttnArgs a, int32_t rows) {
+__device__ __forceinline__ void joined(const AttnArgs& a, const Header& h, const Request& rq, uint32_t row, int32_t token, int lane,
+                                       float l, const float (&o)[D / 64]) {
   constexpr int E = D / 64;
+  const float inv = l == 0.0f ? 0.0f : scale_of<C>(a.vs) / l;
+  uint16_t* op = a.out + (int64_t)token * a.out_ts + (int64_t)head_of(a, rq, h.kv_head, row) * a.out_hs + lane * E;
+  if constexpr (E == 1) {
+    *op = (uint16_t)pack_out<BF16>(o[0] * inv, 0.0f);
+  } else if constexpr (E == 2) {
+    *reinterpret_cast<uint32_t*>(op) = pack_out<BF16>(o[0] * inv, o[1] * inv);
+  } else {
+    *reinterpret_cast<u32x2*>(op) = u32x2{pack_out<BF16>(o[0] * inv, o[1] * inv), pack_out<BF16>(o[2] * inv, o[3] * inv)};
+  }
+}
+
+// Joins the pieces of the items that were shared out.  Blocks (x, ., z) look after kHeaders workers that follow one another
+// (eight workgroups apart, as worker_of numbers them) and the items that begin in one of their shares and end in a later
+// one's; they run on the XCD that wrote the pieces.  With few pieces a wavefront takes a whole row and a block four; with
+// more (one long request over all workers) a block takes one row and its wavefronts a quarter of the pieces each.
+// most: rows of a tile as far as the caller told.
+//
+// A chain of two waits: the headers, then everything else.  Measured, after a block for each header and row that waited for
+// lengths and weights before pieces: 128 items of 48 rows of 128 dims, 4 pieces each, 22 -> 7 us; 256 of 6 rows of 256 dims 6.3
+// -> 4.9; 192 tiles of 256 rows of 256 dims 57 -> 33.  Blocks that ran on any XCD: 8 us where these take 5.6.
+constexpr int kHeaders = 4;
+
+template <Cache C, int D, bool BF16>
+__global__ void __launch_bounds__(kThreads) attention_join_kernel(AttnArgs a, int32_t rows, int32_t most) {
+  constexpr int E = D / 64, kAlone = 16, kAtOnce = 8;
   __shared__ float sums[kWaves][D + 1];
-  const Header h = reinterpret_cast<const Header*>(a.headers)[blockIdx.x];
-  if (h.last_worker < 0) return;
-  const Request rq = request_of(a, h.r);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int32_t n = h.last_worker - h.worker + 1;
-  const bool alone = n <= 16;  // a wavefront joins a row by itself
-  const int32_t per = alone ? kWaves : 1;
-  for (int32_t first = (int32_t)blockIdx.y * per; first < rows; first += (int32_t)gridDim.y * per) {
-    const int32_t local = alone ? first + wave : first;
-    const uint32_t row = (uint32_t)(h.tile * rows + local);
-    const int32_t token = token_of(a, rq, row);
-    if (!alone && token < 0) return;  // the same in all wavefronts; so are later rows
-    if (token < 0) continue;
-    float m = kNoScore;
-    for (int32_t k = lane; k < n; k += 64)
-      m = __builtin_fmaxf(m, a.part_ml[2 * (part_slot((uint32_t)(h.worker + k), k == 0) * rows + local)]);
+  const Header* headers = reinterpret_cast<const Header*>(a.headers) + (blockIdx.x + 8 * kHeaders * blockIdx.z);
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int32_t fours = (most + kWaves - 1) / kWaves, block = (int32_t)blockIdx.y;
+  // lane 8 k + i: word i of header k
+  static_assert(sizeof(Header) == 32 && kHeaders <= 8, "a wavefront's lanes hold the headers");
+  const int32_t words = reinterpret_cast<const int32_t*>(headers + 8 * (lane / 8 % kHeaders))[lane % 8];
+#pragma unroll 1
+  for (int k = 0; k < kHeaders; ++k) {
+    const auto word = [&](int i) { return __builtin_amdgcn_readlane(words, 8 * k + i); };
+    const Header h = {word(0), word(1), word(2), word(3), word(4), {0, 0, 0}};
+    if (h.last_worker < 0) continue;
+    const int32_t w0 = h.worker, n = h.last_worker - w0 + 1;
+    if (n <= kAlone) {
+      // a block's place among fours of rows, which go on from one header to the next where blocks enough were launched
+      int32_t four = (int32_t)gridDim.y > fours ? block - k * fours : block;
+      if (four < 0 || four >= fours) continue;
+      for (;; four += fours) {
+        // All that is read depends on the header alone and is requested at once; rows that the item does not have read
+        // what the workspace holds there and are not written.
+        const int32_t local = four * kWaves + wave, mine = min(lane & (kAlone - 1), n - 1);
+        const f32x2 ml = *reinterpret_cast<const f32x2*>(a.part_ml + 2 * (part_slot((uint32_t)(w0 + mine), mine == 0) * rows + local));
+        float o[E], l = 0.0f, f = 0.0f;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) m = __builtin_fmaxf(m, __shfl_xor(m, d));
-    float o[E], l;
-    const int32_t share = (n + kWaves - 1) / kWaves;
-    join_pieces<D>(a, h, rows, local, alone ? 0 : min(wave * share, n), alone ? n : min((wave + 1) * share, n), m, lane, l, o);
-    if (!alone) {
+        for (int e = 0; e < E; ++e) o[e] = 0.0f;
+#pragma unroll 1
+        for (int32_t b = 0; b < n; b += kAtOnce) {
+          float v[kAtOnce][E];
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i) {
+            const int32_t at = min(b + i, n - 1);  // past the last piece the last again, not added
+            const float* p = a.part + (part_slot((uint32_t)(w0 + at), at == 0) * rows + local) * D + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[i][e] = p[e];
+          }
+          if (b == 0) {
+            float m = ml.x;
+#pragma unroll
+            for (int d = 1; d < kAlone; d <<= 1) m = __builtin_fmaxf(m, __shfl_xor(m, d));
+            f = exp2_of(ml.x - m);
+          }
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i) {
+            const bool there = b + i < n;
+            const float fk = __shfl(f, b + i), lk = __shfl(ml.y, b + i);
+            l = there ? __builtin_fmaf(lk, fk, l) : l;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = there ? __builtin_fmaf(v[i][e], fk, o[e]) : o[e];
+          }
+        }
+        const Request rq = request_of(a, h.r);
+        const uint32_t row = (uint32_t)(h.tile * rows + local);
+        const int32_t token = token_of(a, rq, row);
+        if (token >= 0) joined<C, D, BF16>(a, h, rq, row, token, lane, l, o);
+        const int32_t next = (four + fours) * kWaves;
+        if (next >= rows || token_of(a, rq, (uint32_t)(h.tile * rows + next)) < 0) break;
+      }
+      continue;
+    }
+    const Request rq = request_of(a, h.r);
+    for (int32_t local = block; local < rows; local += (int32_t)gridDim.y) {
+      const uint32_t row = (uint32_t)(h.tile * rows + local);
+      const int32_t token = token_of(a, rq, row);
+      if (token < 0) break;  // the same in all wavefronts; so are later rows
+      float m = kNoScore;
+      for (int32_t i = lane; i < n; i += 64)
+        m = __builtin_fmaxf(m, a.part_ml[2 * (part_slot((uint32_t)(w0 + i), i == 0) * rows + local)]);
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) m = __builtin_fmaxf(m, __shfl_xor(m, d));
+      float o[E], l;
+      const int32_t share = (n + kWaves - 1) / kWaves;
+      join_pieces<D>(a, h, rows, local, min(wave * share, n), min((wave + 1) * share, n), m, lane, l, o);
 #pragma unroll
       for (int e = 0; e < E; ++e) sums[wave][lane * E + e] = o[e];
       if (lane == 0) sums[wave][D] = l;
@@ -682,16 +775,7 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(AttnArgs a, in
         for (int e = 0; e < E; ++e) o[e] += sums[w][lane * E + e];
       }
       __syncthreads();
-      if (wave != 0) continue;
-    }
-    const float inv = l == 0.0f ? 0.0f : scale_of<C>(a.vs) / l;
-    uint16_t* op = a.out + (int64_t)token * a.out_ts + (int64_t)head_of(a, rq, h.kv_head, row) * a.out_hs + lane * E;
-    if constexpr (E == 1) {
-      *op = (uint16_t)pack_out<BF16>(o[0] * inv, 0.0f);
-    } else if constexpr (E == 2) {
-      *reinterpret_cast<uint32_t*>(op) = pack_out<BF16>(o[0] * inv, o[1] * inv);
-    } else {
-      *reinterpret_cast<u32x2*>(op) = u32x2{pack_out<BF16>(o[0] * inv, o[1] * inv), pack_out<BF16>(o[2] * inv, o[3] * inv)};
+      if (wave == 0) joined<C, D, BF16>(a, h, rq, row, token, lane, l, o);
     }
   }
 }
@@ -721,13 +805,18 @@ hipError_t launch_all(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) 
       if (t != hipSuccess) return t;
       break;
     }
+    case AttnKernel::Stream48:
+      if constexpr (C == Cache::Fp4 && D <= 128) launch_stream<C, D, BF16, 3>(a, stream);
+      break;
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.workers == 0) return e;
-  // enough blocks for the rows that a tile has as far as the caller told, one row or four a block; the
-  // kernel's stride covers the others
-  const uint32_t y = (uint32_t)(p.join_rows <= 16 ? p.join_rows : (p.join_rows + kWaves - 1) / kWaves);
-  hipLaunchKernelGGL((attention_join_kernel<C, D, BF16>), dim3((uint32_t)a.workers, y), dim3(kThreads), 0, stream, a, p.rows);
+  // blocks for the rows that a tile has as far as the caller told (the kernel's strides cover the others), four a block, and
+  // where these are few for every header by itself
+  const int32_t fours = (p.join_rows + kWaves - 1) / kWaves, blocks = p.join_rows <= 16 ? kHeaders * fours : fours;
+  static_assert(kComputeUnits % (8 * kHeaders) == 0, "workers come in multiples of the compute units");
+  const dim3 grid(8, (uint32_t)blocks, (uint32_t)(a.workers / (8 * kHeaders)));
+  hipLaunchKernelGGL((attention_join_kernel<C, D, BF16>), grid, dim3(kThreads), 0, stream, a, p.rows, p.join_rows);
   return hipGetLastError();
 }
 

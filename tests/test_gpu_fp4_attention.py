@@ -46,6 +46,34 @@ def test_prompts(new, head_dim):
     check(p, f"prompt {new} D={head_dim}")
 
 
+@pytest.mark.parametrize("new,heads,kv_heads", [(11, 3, 1), (12, 8, 2), (48, 2, 2), (13, 10, 2), (24, 4, 1), (33, 4, 2), (9, 14, 2)])
+@pytest.mark.parametrize("head_dim,dtype", [(64, "bf16"), (128, "f16"), (128, "bf16"), (256, "bf16")])
+@pytest.mark.parametrize("ctx", [40, 1500])
+def test_between_the_row_tiles(new, heads, kv_heads, head_dim, dtype, ctx):
+    """33 to 48 rows in one tile and 65 to 96 in two (of 48, by the bound of the lengths, and of 32 without it); the
+    second request fills a tile in part, the third has no token."""
+    lens = [(ctx, new), (ctx // 3, new // 2), (ctx, 0), (0, new)]
+    p = Problem4(lens, heads, kv_heads, head_dim, dtype=dtype, seed=new + ctx)
+    check(p, f"{new} x {heads}/{kv_heads} D={head_dim} ctx={ctx}")
+    check(p, f"{new} x {heads}/{kv_heads} D={head_dim} ctx={ctx}, long", max_seq_len=5000)
+    if head_dim == 128 and dtype == "bf16":
+        p.options["softcap"] = 20.0
+        p.options["slopes"] = np.linspace(0.0, 0.3, heads, dtype=np.float32)
+        check(p, f"{new} x {heads}/{kv_heads} with a cap and a bias, ctx={ctx}", max_seq_len=5000)
+        p.options["softcap"] = 200.0
+        check(p, f"{new} x {heads}/{kv_heads} with a wide cap and a bias, ctx={ctx}", max_seq_len=5000)
+        del p.options["softcap"], p.options["slopes"]
+    if head_dim <= 128:
+        p.options["tree_mask"] = tree_mask(p.rng, [n for _, n in lens])
+        check(p, f"{new} x {heads}/{kv_heads} trees, ctx={ctx}", max_seq_len=5000)
+
+
+def test_more_tiles_than_are_shared_out():
+    """1040 items of 36 rows: a workgroup for each."""
+    p = Problem4([(3 + r % 50, 9 - r % 3) for r in range(130)], 32, 8, 64, seed=5)
+    check(p, "130 requests, 36 rows", max_seq_len=5000)
+
+
 @pytest.mark.parametrize("block_size", [1, 3, 16, 48, 64, 1000])
 def test_block_sizes_and_ragged_batch(block_size):
     lens = [(0, 0), (77, 5), (0, 31), (500, 1), (0, 0), (200, 12), (3, 0)]
