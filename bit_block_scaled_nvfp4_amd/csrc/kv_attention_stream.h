@@ -33,7 +33,7 @@
 // that one conversion gives a dim's two keys side by side and one packed product gives both their scales.  The codes take half
 // the registers, so that two workgroups of 256 dims share a compute unit, and up to 128 dims a tile may have 48 rows.
 // Measured: 64 requests x up to 8000 positions, one token each, 24 heads over 4 of 256 dims, 321 MB: 74 us and 5 for the
-// join, 4.3 TB/s; half of its time is vector instructions (70 a product of 16 x 16 x 32 at 16 rows), the rest waits.  Forming
+// join, 4.3 TB/s; half of its time is vector instructions (21 for each matrix instruction), the rest waits.  Forming
 // the rows' addresses by scalar instructions where blocks hold a multiple of 16 positions took 75 us, and requesting keys
 // without a condition (so that the wait for values is not one for them too) 76; 16 trees of 12 tokens with 4 heads each over
 // 6001 positions of 128 dims 44 us with both, 45 without: left out.

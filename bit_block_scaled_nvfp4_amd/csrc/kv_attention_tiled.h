@@ -26,6 +26,10 @@
 // no bank conflicts.  Tiles with half their rows empty take as long as full ones: with one wavefront a
 // SIMD its own chain (operand reads, scores, softmax, output) shows in full.  The loop's time depends on its
 // address modulo 32 (chunk of 2048 over 30011 with a bias: 964 to 1030 us over the eight places).
+//
+// Over the 4-bit cache staging costs more: a load for the codes and one for the scale of each piece, a product with the scale,
+// and for keys in BF16, which has no packed product, a step by way of FP32.  Chunk of 2048 over 30011, 24 heads of 256 dims over
+// 4 KV heads: 1.79 ms and 34 us for the join, 0.82 PFLOP/s, the matrix cores busy 38 % of the time.
 #pragma once
 
 #include "kv_attention_common.h"
@@ -141,8 +145,8 @@ struct Fetched {
 struct Fetched4 {
   uint32_t k[2];  // a block of 16 dims of one key
   uint32_t ks;    // its scale
-  uint32_t v[4];  // 4 dims of 4 consecutive keys
-  uint32_t vs[4];  // the scales of the block that holds these dims
+  uint32_t v[2];  // 8 dims of 2 consecutive keys
+  uint32_t vs[2];  // the scales of the block that holds these dims
 };
 
 template <Cache C>
@@ -162,6 +166,15 @@ template <int D>
 __device__ __forceinline__ int v_quad(int lane, int wave) { return (lane & 3) + 4 * (wave % (kKeys<D> / 16)); }
 template <int D>
 __device__ __forceinline__ int v_dim(int lane, int wave) { return 4 * ((lane >> 2) + 16 * (wave / (kKeys<D> / 16))); }
+
+// The 4-bit cache's: a pair of keys and 8 dims.  The 32 lanes of half a store, 8 pairs of keys and 4 eights of dims, touch
+// all of the LDS banks once, and 8 lanes read 32 bytes of a row.  (4 keys and 4 dims, as above, are eight loads where these
+// are four: chunk of 2048 over 30011, 32 heads over 8 of 128 dims 1290 us, so 1202; of 64 dims 824 and 799; 24 over 4 of 256
+// dims 1878 and 1830.)
+template <int D>
+__device__ __forceinline__ int v_pair(int lane, int wave) { return (lane & 7) + 8 * (wave % (kKeys<D> / 16)); }
+template <int D>
+__device__ __forceinline__ int v_dim8(int lane, int wave) { return 8 * ((lane >> 3) + 8 * (wave / (kKeys<D> / 16))); }
 
 // Slots of a tile (`sl`, in LDS) and which of them are in the cache; the codes are requested.
 template <int D>
@@ -187,18 +200,18 @@ __device__ __forceinline__ void fetch(const AttnArgs& a, const int32_t* sl, cons
                                       const uint8_t* vbase, int tid, Fetched4& f, There<D>& there) {
   const int lane = tid & 63, wave = tid >> 6;
   const uint64_t sk = (uint32_t)max(sl[k_key<D>(tid)], 0);
-  const i32x4 sv = *reinterpret_cast<const i32x4*>(sl + 4 * v_quad<D>(lane, wave));
+  const int64_t sv = *reinterpret_cast<const int64_t*>(sl + 2 * v_pair<D>(lane, wave));
   there.lo = uniform64(in_cache[0]);
   if constexpr (D == 64) there.hi = uniform64(in_cache[1]);
   const u32x2 k = *reinterpret_cast<const u32x2*>(kbase + sk * (D / 2) + 8 * k_chunk<D>(tid));
   f.k[0] = k.x;
   f.k[1] = k.y;
   f.ks = a.kbs[sk * (D / 16) + k_chunk<D>(tid)];
-  const int dim = v_dim<D>(lane, wave);
+  const uint32_t dim = v_dim8<D>(lane, wave);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint64_t row = (uint32_t)max(sv[i], 0);
-    f.v[i] = *reinterpret_cast<const uint16_t*>(vbase + row * (D / 2) + dim / 2);
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t row = (uint32_t)max((int32_t)(sv >> (32 * i)), 0);
+    f.v[i] = *reinterpret_cast<const uint32_t*>(vbase + row * (D / 2) + dim / 2);
     f.vs[i] = a.vbs[row * (D / 16) + dim / 16];
   }
 }
@@ -250,16 +263,21 @@ __device__ __forceinline__ bool stage(const Fetched4& f, const There<D>&, bool, 
 #pragma unroll
   for (int e = 0; e < 2; ++e)
     *reinterpret_cast<u32x4*>(kt + k_offset<D>(kk, 2 * c + (e ^ odd))) = decode_key8<BF16>(e ^ odd ? k1 : k0, f.ks, 0);
-  const int quad = v_quad<D>(lane, wave), dim = v_dim<D>(lane, wave);
-  // dims 0 and 2 of keys 0 and 1, then of keys 2 and 3; dims 1 and 3
+  const int pair = v_pair<D>(lane, wave), dim = v_dim8<D>(lane, wave);
   uint32_t even, odds;
-  pair_keys(f.v[0] | f.v[2] << 16, f.v[1] | f.v[3] << 16, even, odds);
-  const f16x2 s01 = scales_of_keys(f.vs[0], f.vs[1]), s23 = scales_of_keys(f.vs[2], f.vs[3]);
-  const int gr = (quad >> 2) * 2 + (quad & 1), half = (quad >> 1) & 1;
-  *reinterpret_cast<u32x2*>(vt + v_offset<D>(dim, gr) + 8 * half) = u32x2{two_f16<0>(even, s01), two_f16<2>(even, s23)};
-  *reinterpret_cast<u32x2*>(vt + v_offset<D>(dim + 1, gr) + 8 * half) = u32x2{two_f16<0>(odds, s01), two_f16<2>(odds, s23)};
-  *reinterpret_cast<u32x2*>(vt + v_offset<D>(dim + 2, gr) + 8 * half) = u32x2{two_f16<1>(even, s01), two_f16<3>(even, s23)};
-  *reinterpret_cast<u32x2*>(vt + v_offset<D>(dim + 3, gr) + 8 * half) = u32x2{two_f16<1>(odds, s01), two_f16<3>(odds, s23)};
+  pair_keys(f.v[0], f.v[1], even, odds);
+  const f16x2 by = scales_of_keys(f.vs[0], f.vs[1]);
+  // (granules as in the other stage)
+  const int quad = pair >> 1, gr = (quad >> 2) * 2 + (quad & 1), at = 8 * ((quad >> 1) & 1) + 4 * (pair & 1);
+  const auto put = [&](int d, uint32_t two) { *reinterpret_cast<uint32_t*>(vt + v_offset<D>(dim + d, gr) + at) = two; };
+  put(0, two_f16<0>(even, by));
+  put(1, two_f16<0>(odds, by));
+  put(2, two_f16<1>(even, by));
+  put(3, two_f16<1>(odds, by));
+  put(4, two_f16<2>(even, by));
+  put(5, two_f16<2>(odds, by));
+  put(6, two_f16<3>(even, by));
+  put(7, two_f16<3>(odds, by));
   return false;
 }
 
