@@ -110,8 +110,9 @@ def _meet(a, b):
             if max(wide, far) <= pitch and begin >= wide and begin + far <= pitch:
                 return False
     torch = _base._torch()
-    mine = torch.unique((p + torch.arange(T)[:, None] * ts + torch.arange(H)[None, :] * hs).flatten())
-    its = (q + torch.arange(U)[:, None] * us + torch.arange(G)[None, :] * gs).flatten()
+    upto = functools.partial(torch.arange, device="cpu")
+    mine = torch.unique((p + upto(T)[:, None] * ts + upto(H)[None, :] * hs).flatten())
+    its = (q + upto(U)[:, None] * us + upto(G)[None, :] * gs).flatten()
     place = torch.searchsorted(mine, its)  # the vectors before and behind each one
     before, behind = mine[(place - 1).clamp(min=0)], mine[place.clamp(max=len(mine) - 1)]
     return bool((((its >= before) & (its < before + w)) | ((behind >= its) & (behind < its + x))
@@ -120,8 +121,10 @@ def _meet(a, b):
 
 def _turn(positions, inv_freq, tokens, head_dim, device, interleaved, step, torch):
     """Arguments of the rotation: positions, frequencies, their number, the flag."""
-    if interleaved is not False and interleaved is not True and interleaved not in (0, 1):
-        raise ValueError(f"interleaved must be True or False, got {interleaved!r}")
+    if interleaved is not False and interleaved is not True:
+        if interleaved not in (0, 1):
+            raise ValueError(f"interleaved must be True or False, got {interleaved!r}")
+        interleaved = int(interleaved)
     if positions is None or inv_freq is None:
         if positions is not None or inv_freq is not None:
             raise ValueError("positions and inv_freq come together")
@@ -206,8 +209,8 @@ def nvfp4_qk_norm_rope(q, k=None, positions=None, inv_freq=None, *, q_weight=Non
     if ((qo < q_end and qp < qo_end) or (ko_end and (kp < ko_end and ko < k_end or qp < ko_end and ko < q_end or ko < qo_end and qo < ko_end))
             or (kp is not None and kp < qo_end and qo < k_end)):
         _refuse_meeting(q, q_strides, k, k_strides, q_out if qo_end else None, qo_strides, k_out if ko_end else None, ko_strides)
-    _call(dev, lib.nvfp4_qk_norm_rope, qp, H, *q_strides, kp, Hk, *k_strides, code, T, D, p, f, n, pairs, qw, kw, wt, eps,
-          weight_offset, qo, *qo_strides, ko, *ko_strides)
+    _call(dev, lib.nvfp4_qk_norm_rope, qp, H, *q_strides, kp, Hk, *k_strides, code, T, D, p, f, n, pairs, qw, kw, wt, float(eps),
+          float(weight_offset), qo, *qo_strides, ko, *ko_strides)
     return q_out, k_out
 
 
@@ -260,7 +263,7 @@ def _append(key, value, positions, inv_freq, k_scale, v_scale, scale_names, slot
             raise ValueError(f"{name} must be one float32 value on {dev}")
     sm = None if slots is None else _vector(slots, T, torch.int64, dev, "slot_mapping")
     k, v, size = key.data_ptr(), value.data_ptr(), 4 if code == _base.NVFP4_F32 else 2
-    args = (k, v, code, T, Hk, D, *k_strides, *v_strides, p, f, n, pairs, kw, wt, eps, weight_offset,
+    args = (k, v, code, T, Hk, D, *k_strides, *v_strides, p, f, n, pairs, kw, wt, float(eps), float(weight_offset),
             k_scale.data_ptr(), v_scale.data_ptr(), sm)
     ke, ve = k + _extent(shape, k_strides, size), v + _extent(shape, v_strides, size)
     if k < ve and v < ke:  # (of one fused row: one range)
@@ -456,7 +459,7 @@ def _attention(fn, q, key_codes, key_scales, value_codes, value_scales, key_gsca
     _call(dev, fn, q.data_ptr(), _base.NVFP4_BF16 if dtype is torch.bfloat16 else _base.NVFP4_F16,
           T, H, Hk, D, q_ts, q_hs, key_codes.data_ptr(), key_scales.data_ptr(), value_codes.data_ptr(),
           value_scales.data_ptr(), key_gscale.data_ptr(), value_gscale.data_ptr(), B, bs, block_table.data_ptr(), R, W,
-          table_ld, qs, sl, D ** -0.5 if scale is None else scale, softcap, sp, *extra(T, R, dev),
+          table_ld, qs, sl, D ** -0.5 if scale is None else float(scale), float(softcap), sp, *extra(T, R, dev),
           max_query_len, max_seq_len, out.data_ptr(), out_ts, out_hs, None if ws is None else ws.data_ptr(), need)
     return out
 

@@ -421,3 +421,16 @@ def test_side_stream_and_captured_graphs():
         step(q2, k2, b)
         torch.cuda.synchronize()
         assert torch.equal(qo, q2) and torch.equal(ko, k2) and all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_numbers_of_other_types_are_taken():
+    """numpy's scalars for the numbers and the flag give what Python's give."""
+    import torch
+
+    c = Case(5, 4, 2, 64, 16, weights="f32", interleaved=True, eps=0.125, offset=0.5)
+    d = dict(positions=torch.from_numpy(c.positions).to(torch.int32).to(DEV), inv_freq=_up(c.inv_freq), q_weight=_up(c.qw), k_weight=_up(c.kw))
+    q, k = _up(c.q, c.dtype), _up(c.k, c.dtype)
+    log("numpy scalars")
+    want = nv.nvfp4_qk_norm_rope(q, k, **d, eps=0.125, weight_offset=0.5, interleaved=True)
+    got = nv.nvfp4_qk_norm_rope(q, k, **d, eps=np.float32(0.125), weight_offset=np.float64(0.5), interleaved=np.True_)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
