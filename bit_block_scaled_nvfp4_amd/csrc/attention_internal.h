@@ -58,6 +58,7 @@ struct AttnPlan {
   int32_t row_tiles;  // of the longest request as far as the caller told (grid bound)
   int32_t all_tiles;  // > 0 (tiled kernel without workers): the grid counts row tiles of all requests
   int64_t workspace;
+  bool wide;  // streaming kernels over the 4-bit cache, without workers: workgroups of twice as many wavefronts
 };
 
 struct AttnArgs {

@@ -47,10 +47,10 @@ namespace {
 using namespace attn;
 
 constexpr int kThreads = 256;
-constexpr int kWaves = 4;
-constexpr int kStep = 32;              // positions of a wavefront's step
-constexpr int kUnit = kWaves * kStep;  // positions of a workgroup's step
-static_assert(kUnit == kStreamUnit, "the division of the work counts in these");
+constexpr int kWaves = 4;      // of a workgroup
+constexpr int kWideWaves = 8;  // of the wide form's, over the 4-bit cache
+constexpr int kStep = 32;  // positions of a wavefront's step
+static_assert(kWaves * kStep == kStreamUnit, "the division of the work counts in a workgroup's steps");
 
 // Codes of 32 positions as a lane holds them.
 template <Cache C, int D>
@@ -424,10 +424,10 @@ __device__ __forceinline__ void step(const Segment& sg, const Request& rq, const
   }
 }
 
-template <Cache C, int D, bool BF16, int NQ, Scores SCORES>
+template <Cache C, int D, bool BF16, int NQ, Scores SCORES, int W>
 __device__ __forceinline__ void segment(const Segment& sg, bool split, int32_t worker, float* lds, u32x4* queries) {
   const AttnArgs& a = args();
-  constexpr int kRows = 16 * NQ;
+  constexpr int kRows = 16 * NQ, kUnit = W * kStep;
   constexpr int kPitch = D + 4;  // floats; 16 bytes a row apart, so a store's 8 lanes differ in banks
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int g = lane >> 4, d16 = lane & 15;
@@ -451,7 +451,7 @@ __device__ __forceinline__ void segment(const Segment& sg, bool split, int32_t w
     const uint16_t* qp = a.q + (int64_t)w.token * a.q_ts + (int64_t)w.head * a.q_hs + g * (C == Cache::Fp4 ? D / 4 : 16);
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) {
-      if (kQueriesInLds<C, D, NQ> && (n * (D / 32) + j) % kWaves != wave) continue;
+      if (kQueriesInLds<C, D, NQ> && (n * (D / 32) + j) % W != wave) continue;
       const u32x4 q = w.token >= 0 ? *reinterpret_cast<const u32x4*>(qp + (C == Cache::Fp4 ? 8 * j : 64 * (j >> 1) + 8 * (j & 1))) : u32x4{0, 0, 0, 0};
       if constexpr (kQueriesInLds<C, D, NQ>) queries[(n * (D / 32) + j) * 64 + lane] = q;
       else s.q[n][j] = q;
@@ -529,7 +529,7 @@ __device__ __forceinline__ void segment(const Segment& sg, bool split, int32_t w
 
   // join the wavefronts
   const AttnArgs& ea = args();
-  float* ml = lds + kWaves * 16 * kPitch;  // [wave][kRows][2]
+  float* ml = lds + W * 16 * kPitch;  // [wave][kRows][2]
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     const float l = sum_over_groups(s.l[n]);
@@ -544,7 +544,7 @@ __device__ __forceinline__ void segment(const Segment& sg, bool split, int32_t w
     __syncthreads();
     float m = kNoScore;
 #pragma unroll
-    for (int k = 0; k < kWaves; ++k) m = __builtin_fmaxf(m, ml[(k * kRows + 16 * n + d16) * 2]);
+    for (int k = 0; k < W; ++k) m = __builtin_fmaxf(m, ml[(k * kRows + 16 * n + d16) * 2]);
     const float f = exp2_of(s.m[n] - m);
     float* mine = lds + (wave * 16 + d16) * kPitch + g * (D / 4);
 #pragma unroll
@@ -557,18 +557,19 @@ __device__ __forceinline__ void segment(const Segment& sg, bool split, int32_t w
     __syncthreads();
     // 16 threads a row, D / 16 contiguous dims each
     const int row = tid >> 4, part = tid & 15;
+    if (W > 4 && row >= 16) continue;
     float mr = kNoScore, lr = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kWaves; ++k) mr = __builtin_fmaxf(mr, ml[(k * kRows + 16 * n + row) * 2]);
+    for (int k = 0; k < W; ++k) mr = __builtin_fmaxf(mr, ml[(k * kRows + 16 * n + row) * 2]);
 #pragma unroll
-    for (int k = 0; k < kWaves; ++k)
+    for (int k = 0; k < W; ++k)
       lr += ml[(k * kRows + 16 * n + row) * 2 + 1] * exp2_of(ml[(k * kRows + 16 * n + row) * 2] - mr);
     float o[D / 16];
 #pragma unroll
     for (int t = 0; t < D / 16; t += 4) {
       f32x4 sum = *reinterpret_cast<f32x4*>(lds + row * kPitch + part * (D / 16) + t);
 #pragma unroll
-      for (int k = 1; k < kWaves; ++k)
+      for (int k = 1; k < W; ++k)
         sum += *reinterpret_cast<f32x4*>(lds + (k * 16 + row) * kPitch + part * (D / 16) + t);
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[t + i] = sum[i];
@@ -595,14 +596,13 @@ __device__ __forceinline__ void segment(const Segment& sg, bool split, int32_t w
   __syncthreads();  // the next segment writes ml and the tiles again
 }
 
-template <Cache C, int D, bool BF16, int NQ, Scores SCORES>
-__global__ void __launch_bounds__(kThreads, C == Cache::Fp4 ? stream_groups_fp4(D, 16 * NQ) : stream_groups(D, 16 * NQ)) attention_stream_kernel(AttnArgs) {
-  constexpr int kRows = 16 * NQ;
-  __shared__ __align__(16) float lds[kWaves * 16 * (D + 4) + kWaves * kRows * 2];
+template <Cache C, int D, bool BF16, int NQ, Scores SCORES, int W>
+__global__ void __launch_bounds__(64 * W, W > kWaves ? W / kWaves : C == Cache::Fp4 ? stream_groups_fp4(D, 16 * NQ) : stream_groups(D, 16 * NQ)) attention_stream_kernel(AttnArgs) {
+  constexpr int kRows = 16 * NQ, kUnit = W * kStep;
+  __shared__ __align__(16) float lds[W * 16 * (D + 4) + W * kRows * 2];
   __shared__ u32x4 queries[kQueriesInLds<C, D, NQ> ? NQ * (D / 32) * 64 : 1];
-  __shared__ Share<kThreads> share;
   Segment s;
-  if (args().workers == 0) {
+  if (W > kWaves || args().workers == 0) {
     const AttnArgs& a = args();
     s.kv_head = blockIdx.x;
     s.r = blockIdx.y;
@@ -612,15 +612,16 @@ __global__ void __launch_bounds__(kThreads, C == Cache::Fp4 ? stream_groups_fp4(
     s.u0 = 0;
     s.u1 = (int32_t)(((uint32_t)q.keys + kUnit - 1) / kUnit);
     const int32_t tiles = (int32_t)(((uint32_t)q.count * a.group.d + kRows - 1) / kRows);
-    for (s.tile = blockIdx.z; s.tile < tiles; s.tile += gridDim.z) segment<C, D, BF16, NQ, SCORES>(s, false, 0, lds, queries);
+    for (s.tile = blockIdx.z; s.tile < tiles; s.tile += gridDim.z) segment<C, D, BF16, NQ, SCORES, W>(s, false, 0, lds, queries);
     return;
   }
+  __shared__ Share<64 * W> share;
   share.begin(kRows, kUnit);
   Header* header = reinterpret_cast<Header*>(args().headers) + blockIdx.x;
   if (threadIdx.x == 0) header->last_worker = -1;
   while (share.next(kRows, kUnit, s)) {
     if (s.first && !s.last && threadIdx.x == 0) *header = Header{s.r, s.tile, s.kv_head, s.last_worker, share.worker, {0, 0, 0}};
-    segment<C, D, BF16, NQ, SCORES>(s, true, uniform(share.worker), lds, queries);
+    segment<C, D, BF16, NQ, SCORES, W>(s, true, uniform(share.worker), lds, queries);
   }
 }
 
@@ -780,26 +781,42 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(AttnArgs a, in
   }
 }
 
-template <Cache C, int D, bool BF16, int NQ, Scores SCORES>
+template <Cache C, int D, bool BF16, int NQ, Scores SCORES, int W>
 void launch_stream(const AttnArgs& a, hipStream_t stream) {
   const dim3 grid = a.workers ? dim3((uint32_t)a.workers) : dim3((uint32_t)a.kv_heads, (uint32_t)a.requests, (uint32_t)a.row_tiles);
-  hipLaunchKernelGGL((attention_stream_kernel<C, D, BF16, NQ, SCORES>), grid, dim3(kThreads), 0, stream, a);
+  hipLaunchKernelGGL((attention_stream_kernel<C, D, BF16, NQ, SCORES, W>), grid, dim3(64 * W), 0, stream, a);
 }
 
-template <Cache C, int D, bool BF16, int NQ>
+template <Cache C, int D, bool BF16, int NQ, int W = kWaves>
 void launch_stream(const AttnArgs& a, hipStream_t stream) {
   switch (scores_of(a)) {
-    case Scores::Plain: launch_stream<C, D, BF16, NQ, Scores::Plain>(a, stream); break;
-    case Scores::Modified: launch_stream<C, D, BF16, NQ, Scores::Modified>(a, stream); break;
-    case Scores::WideCap: launch_stream<C, D, BF16, NQ, Scores::WideCap>(a, stream); break;
+    case Scores::Plain: launch_stream<C, D, BF16, NQ, Scores::Plain, W>(a, stream); break;
+    case Scores::Modified: launch_stream<C, D, BF16, NQ, Scores::Modified, W>(a, stream); break;
+    case Scores::WideCap: launch_stream<C, D, BF16, NQ, Scores::WideCap, W>(a, stream); break;
   }
 }
 
 template <Cache C, int D, bool BF16>
 hipError_t launch_all(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
   switch (p.kernel) {
-    case AttnKernel::Stream16: launch_stream<C, D, BF16, 1>(a, stream); break;
-    case AttnKernel::Stream32: launch_stream<C, D, BF16, 2>(a, stream); break;
+    case AttnKernel::Stream16:
+      if constexpr (C == Cache::Fp4 && D <= 128) {
+        if (p.wide) {
+          launch_stream<C, D, BF16, 1, kWideWaves>(a, stream);
+          break;
+        }
+      }
+      launch_stream<C, D, BF16, 1>(a, stream);
+      break;
+    case AttnKernel::Stream32:
+      if constexpr (C == Cache::Fp4 && D == 64) {
+        if (p.wide) {
+          launch_stream<C, D, BF16, 2, kWideWaves>(a, stream);
+          break;
+        }
+      }
+      launch_stream<C, D, BF16, 2>(a, stream);
+      break;
     case AttnKernel::Tiled: {
       const hipError_t t = C == Cache::Fp4 ? launch_attention_tiled_fp4(a, D, BF16, stream) : launch_attention_tiled(a, D, BF16, stream);
       if (t != hipSuccess) return t;

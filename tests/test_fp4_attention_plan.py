@@ -13,8 +13,8 @@ CALL = '''
 #include "attention_internal.h"
 extern "C" void test_plan(int64_t t, int64_t h, int64_t kv, int64_t d, int64_t r, int64_t mq, int64_t ms, int64_t* out) {
   const nvfp4::AttnPlan p = nvfp4::plan_attention_fp4(t, h, kv, d, r, mq < t ? mq : t, ms);
-  const int64_t v[] = {(int64_t)p.kernel, p.rows, p.join_rows, p.workers, p.row_tiles, p.workspace};
-  for (int i = 0; i < 6; ++i) out[i] = v[i];
+  const int64_t v[] = {(int64_t)p.kernel, p.rows, p.join_rows, p.workers, p.row_tiles, p.workspace, p.wide};
+  for (int i = 0; i < 7; ++i) out[i] = v[i];
 }
 '''
 
@@ -33,9 +33,9 @@ def plan(tmp_path_factory):
     fn.restype = None
 
     def get(tokens, heads, kv_heads, head_dim, requests, new, longest):
-        out = (ctypes.c_int64 * 6)()
+        out = (ctypes.c_int64 * 7)()
         fn(tokens, heads, kv_heads, head_dim, requests, new, longest, out)
-        return dict(zip(("kernel", "rows", "join_rows", "workers", "row_tiles", "workspace"), out))
+        return dict(zip(("kernel", "rows", "join_rows", "workers", "row_tiles", "workspace", "wide"), out))
 
     return get
 
@@ -58,3 +58,15 @@ def test_sizes_of_the_gpu_tests_reach_48_rows(plan):
         assert plan(2 * new + new // 2, heads, kv_heads, 128, 4, new, 5000)["rows"] == 48
     p = plan(130 * 8, 32, 8, 64, 130, 9, 5000)
     assert p["rows"] == 48 and p["workers"] == 0
+
+
+@pytest.mark.parametrize("head_dim", [64, 128, 256])
+def test_eight_wavefronts(plan, head_dim):
+    """Where a workgroup has the keys to itself, more than one step of them and a compute unit of its own."""
+    wide = lambda requests, rows, longest: plan(requests * rows, 4, 4, head_dim, requests, rows, longest)["wide"]  # noqa: E731
+    assert bool(wide(1, 1, 500)) == bool(wide(64, 16, 1024)) == bool(wide(64, 1, 257)) == (head_dim <= 128)
+    assert bool(wide(8, 32, 1024)) == bool(wide(8, 40, 1024)) == bool(wide(1, 300, 1024)) == (head_dim == 64)
+    assert not wide(65, 1, 1024) and not wide(1, 1, 256) and not wide(1, 1, 1025) and not wide(64, 300, 1024)
+    for requests, rows, longest in ((3, 7, 500), (300, 1, 500), (3, 7, 5000), (64, 48, 1024)):
+        p = plan(requests * rows, 4, 4, head_dim, requests, rows, longest)
+        assert not (p["wide"] and p["workers"])

@@ -68,10 +68,21 @@ def test_between_the_row_tiles(new, heads, kv_heads, head_dim, dtype, ctx):
         check(p, f"{new} x {heads}/{kv_heads} trees, ctx={ctx}", max_seq_len=5000)
 
 
-def test_more_tiles_than_are_shared_out():
-    """1040 items of 36 rows: a workgroup for each."""
-    p = Problem4([(3 + r % 50, 9 - r % 3) for r in range(130)], 32, 8, 64, seed=5)
-    check(p, "130 requests, 36 rows", max_seq_len=5000)
+@pytest.mark.parametrize("new,head_dim", [(9, 64), (9, 128), (4, 64), (4, 256), (8, 128), (1, 128)])
+@pytest.mark.parametrize("max_seq_len", [None, 5000])
+def test_more_items_than_compute_units(new, head_dim, max_seq_len):
+    """1040 items of up to 36 rows: a workgroup of four wavefronts for each, whatever the bound of the lengths."""
+    p = Problem4([(3 + r % 150, max(1, new - r % 3)) for r in range(130)], 32, 8, head_dim, seed=5)
+    check(p, f"130 requests, {4 * new} rows", max_seq_len=max_seq_len)
+
+
+@pytest.mark.parametrize("new,head_dim", [(1, 64), (1, 128), (1, 256), (4, 256), (8, 64), (8, 128), (8, 256)])
+@pytest.mark.parametrize("longest", [127, 128, 129, 255, 256, 257, 511, 513, 1024])
+def test_few_items_of_few_steps(new, head_dim, longest):
+    """Around the steps of a workgroup of eight wavefronts (256 positions), with requests that end in its first ones and one
+    without a token."""
+    p = Problem4([(longest - new, new), (5, new), (longest // 2, new), (100, 0)], 8, 2, head_dim, seed=longest)
+    check(p, f"{new} tokens over {longest}", max_seq_len=longest)
 
 
 @pytest.mark.parametrize("block_size", [1, 3, 16, 48, 64, 1000])
