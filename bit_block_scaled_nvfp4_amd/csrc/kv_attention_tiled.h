@@ -167,10 +167,10 @@ __device__ __forceinline__ int v_quad(int lane, int wave) { return (lane & 3) + 
 template <int D>
 __device__ __forceinline__ int v_dim(int lane, int wave) { return 4 * ((lane >> 2) + 16 * (wave / (kKeys<D> / 16))); }
 
-// The 4-bit cache's: a pair of keys and 8 dims.  The 32 lanes of half a store, 8 pairs of keys and 4 eights of dims, touch
-// all of the LDS banks once, and 8 lanes read 32 bytes of a row.  (4 keys and 4 dims, as above, are eight loads where these
-// are four: chunk of 2048 over 30011, 32 heads over 8 of 128 dims 1290 us, so 1202; of 64 dims 824 and 799; 24 over 4 of 256
-// dims 1878 and 1830.)
+// The 4-bit cache's: a pair of keys and 8 dims; 8 lanes read 32 bytes of a row.  (4 keys and 4 dims, as above, are eight
+// loads where these are four: chunk of 2048 over 30011, 32 heads over 8 of 128 dims 1290 us, so 1202; of 64 dims 824 and 799; 24
+// over 4 of 256 dims 1878 and 1830.)  A store waits two clocks for banks; 16 pairs and 4 eights of 256 dims a wavefront have
+// no such wait, read 16 bytes of a row, and take as long (1793 and 1800 us).
 template <int D>
 __device__ __forceinline__ int v_pair(int lane, int wave) { return (lane & 7) + 8 * (wave % (kKeys<D> / 16)); }
 template <int D>
@@ -256,9 +256,10 @@ template <int D, bool BF16>
 __device__ __forceinline__ bool stage(const Fetched4& f, const There<D>&, bool, char* kt, char* vt, int tid) {
   const int lane = tid & 63, wave = tid >> 6;
   const int kk = k_key<D>(tid), c = k_chunk<D>(tid);
-  // Granules 2 c and 2 c + 1 of the key: which of them first is chosen so that the 16 lanes of a store, which differ
-  // in c or in the key's low bits, touch 16 different columns
-  const int odd = D == 256 ? c >> 3 & 1 : D == 128 ? kk & 1 : kk >> 1 & 1;
+  // Granules 2 c and 2 c + 1 of the key: which of them first is chosen so that 16 neighbouring lanes of a store, which
+  // differ in c or in the key's low bits, touch 16 different columns, and each 8 of them columns that differ modulo 8 (without
+  // the second, half of the stores' bank conflicts: 1843 us for 1793, at 64 dims 783 for 760)
+  const int odd = (D == 256 ? c >> 2 ^ c >> 3 : D == 128 ? c >> 2 ^ kk : kk ^ kk >> 1) & 1;
   const uint32_t k0 = f.k[0], k1 = f.k[1];
 #pragma unroll
   for (int e = 0; e < 2; ++e)
