@@ -2,8 +2,8 @@
 // Also the kernel that joins partial results.  Kernels are templates over the cache's format; kv_attention.hip
 // has those of the FP8 cache, kv_attention_fp4.hip those of the 4-bit cache.
 //
-// What bounds it: every key and value code is read once per (request, KV head) and used by 16 or
-// 32 rows, so the call is bound by HBM reads.  The kernel therefore keeps as many loads in flight as
+// What bounds it: every key and value code is read once per (request, KV head) and used by 16, 32 or 48
+// rows, so the call is bound by HBM reads.  The kernel therefore keeps as many loads in flight as
 // its registers hold and touches LDS only to join its wavefronts at the end of an item.  A wavefront
 // takes 32 positions at a time, from the cache straight into MFMA operand registers:
 //
