@@ -426,3 +426,11 @@ def test_two_streams_at_once():
         for o in outs[k]:
             assert bool((o == outs[k][0]).all())
         compare(outs[k][0].double().cpu().numpy(), want, tol, f"stream {k}")
+
+
+@pytest.mark.parametrize("head_dim", [64, 256])
+@pytest.mark.parametrize("max_query_len,new", [(1, 6), (3, 9), (None, 40)])
+def test_more_pieces_than_a_wavefront_joins(max_query_len, new, head_dim):
+    """Two long requests over all workgroups: more than 16 pieces an item, and more rows than the bound said."""
+    p = Problem4([(9000, new), (5000, 1)], 8, 2, head_dim, seed=31)
+    check(p, f"{new} tokens said to be {max_query_len}", max_query_len=max_query_len)
