@@ -29,6 +29,16 @@ __device__ __forceinline__ Rows rows_of(const VerifyArgs& a, int32_t r) {
   return Rows{s, max(e, s) - 1};
 }
 
+// Whether a request behind r owns row t too.  That takes starts that fall: the row is then the last such request's, and no
+// other writes it (two writers in no order would leave either's token).
+__device__ bool taken_later(const VerifyArgs& a, int32_t r, int32_t t) {
+  for (int32_t i = r + 2; i < a.requests; ++i) {
+    const Rows q = rows_of(a, i);
+    if (q.start <= t && t <= q.last) return true;
+  }
+  return false;
+}
+
 // First row of the request that goes no further: its drafted token is not accepted, or it is the last.  By every
 // wavefront for itself.
 __device__ __forceinline__ int32_t row_reached(const VerifyArgs& a, const Rows& q) {
@@ -157,6 +167,9 @@ __global__ void __launch_bounds__(kThreads) verify_pick_kernel(VerifyArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int32_t row = q.start + a.accepted[r];
   const double u = a.sample_u[r];
+  // whether a later request starts among this one's rows or before them (the next one starts behind them)
+  bool falls = false;
+  for (int32_t i = r + 2 + tid; i < a.requests; i += kThreads) falls |= a.query_start[i] <= q.last;
   const double* sums = a.sums + (int64_t)r * a.chunks * 2;
   // the row's sum, of the weights or, where they are all zero, of the target's probabilities
   double left = 0.0, whole = 0.0;
@@ -238,7 +251,11 @@ __global__ void __launch_bounds__(kThreads) verify_pick_kernel(VerifyArgs a) {
     // (where rounding leaves the chunk's sum at the aim: its last token with a weight)
     token = at_end || at == kNone ? tail : at;
   }
-  for (int32_t t = q.start + tid; t <= q.last; t += kThreads) a.out[t] = t < row ? a.tokens[t + 1] : t == row ? token : -1;
+  falls = __syncthreads_or(falls);
+  for (int32_t t = q.start + tid; t <= q.last; t += kThreads) {
+    if (__builtin_expect(falls, 0) && taken_later(a, r, t)) continue;
+    a.out[t] = t < row ? a.tokens[t + 1] : t == row ? token : -1;
+  }
 }
 
 }  // namespace

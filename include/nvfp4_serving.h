@@ -197,7 +197,9 @@ int64_t nvfp4_kv_fp4_attention_workspace(int64_t tokens, int64_t heads, int64_t 
  *   value gives -1.
  * Without draft_probs the drafted tokens count as certain: q_i(x_i) = 1, q_i(v) = 0 otherwise.
  *   accepted[r] = a;  out_tokens[s + i] = x_i for i < a, the sampled token for i = a, -1 for a < i <= n.
- * A request without rows has accepted 0.  Entries of out_tokens of no request are left as they were.
+ * A request without rows has accepted 0.  Entries of out_tokens of no request are left as they were.  Starts that fall
+ * leave a request without rows, or rows with several requests: each is verified over all its rows, and the last of
+ * them writes such a row.
  * Sums are formed in binary64 in a fixed order.  NaN probabilities count as 0 weights and are not accepted.
  *
  *   target_probs  device, float [rows, vocab], row pitch target_ld >= vocab (elements); 4-byte aligned.

@@ -255,3 +255,21 @@ def test_side_stream_graphs_and_two_at_once():
         torch.cuda.synchronize()
         for x, y in kept:
             assert torch.equal(x, a) and torch.equal(y, o)
+
+
+@pytest.mark.parametrize("start", [[0, 6, 2, 9, 0, 4, 4, 12, -3, 1], [0, 3, 7, 12, 0, 0, 0], [0, 12, 0, 12, 0, 12], [5, 12, 4, 8, 3, 6, 0, 1]])
+def test_starts_that_fall_leave_a_rows_last_request(start):
+    """Rows of several requests: the last one's tokens, whatever order the workgroups run in."""
+    b = Batch([0] * (len(start) - 1), 9001, seed=12, pad=12 - (len(start) - 1))
+    b.start = np.array(start)
+    for k in range(8):
+        b.u = np.roll(b.u, 1)
+        check(b, f"starts {start}, {k}")
+
+
+def test_starts_that_fall_among_many_requests():
+    b = Batch([0] * 700, 40, seed=13)
+    rng = np.random.default_rng(14)
+    b.start = np.cumsum(rng.integers(-3, 5, 701))  # falls now and then, by less than it rises
+    b.start[300:310] = b.start[300]
+    check(b, "700 requests whose starts fall")

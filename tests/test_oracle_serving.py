@@ -144,3 +144,17 @@ def test_verification_by_hand():
     # certain drafts: 0.6 >= 0.5; the rest without token 1
     assert run([9, 1, 2], [0.6, 0.0, 0.0], 0.9, None) == [[0], [0, -1, -1]]
     assert run([9, 5, 2], [0.0, 0.0, 0.0], 0.9, None) == [[0], [1, -1, -1]]
+
+
+def test_a_row_of_several_requests_is_the_last_ones():
+    rng = np.random.default_rng(5)
+    p, q = (x / x.sum(1, keepdims=True) for x in rng.random((2, 12, 9)).astype(np.float32))
+    tokens, u = rng.integers(0, 9, 12), rng.random(12).astype(np.float32)
+    for start in ([0, 6, 2, 9, 0, 4], [0, 3, 7, 12, 0, 0, 0], [-4, 3, 2, 100]):
+        w = rng.random(len(start) - 1).astype(np.float32)
+        accepted, out = osv.verify(p, q, tokens, start, u, w, np.full(12, -7))
+        alone = [osv.verify(p, q, tokens, start[r:r + 2], u, w[r:r + 1], np.full(12, -7)) for r in range(len(w))]
+        assert accepted.tolist() == [a[0] for a, _ in alone]
+        for t in range(12):
+            owners = [r for r in range(len(w)) if max(start[r], 0) <= t < min(start[r + 1], 12)]
+            assert out[t] == (alone[owners[-1]][1][t] if owners else -7)
