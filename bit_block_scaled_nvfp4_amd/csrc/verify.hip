@@ -187,7 +187,9 @@ __global__ void __launch_bounds__(kThreads) verify_pick_kernel(VerifyArgs a) {
   const bool plain = !(left > 0.0);
   Weights w = weights_of(a, q, row);
   if (plain) w = Weights{w.p, nullptr, -1};
-  const double aim = u * (plain ? whole : left);
+  // (of 1 and more, and NaN: the last token with a weight.  The total, and running sums, added in another order, may lie
+  // either side of one another)
+  const double aim = u < 1.0 ? u * (plain ? whole : left) : __builtin_inf();
   // the first chunk whose sum passes the aim, or the last that has any weight
   int32_t chosen = -1, last = -1;
   double before = 0.0, base = 0.0;

@@ -273,3 +273,30 @@ def test_starts_that_fall_among_many_requests():
     b.start = np.cumsum(rng.integers(-3, 5, 701))  # falls now and then, by less than it rises
     b.start[300:310] = b.start[300]
     check(b, "700 requests whose starts fall")
+
+
+@pytest.mark.parametrize("certain", [False, True])
+@pytest.mark.parametrize("vocab", [4097, 32000])
+def test_numbers_of_one_and_more_take_the_last_token_with_a_weight(vocab, certain):
+    """Wide rows whose second half weighs less than a sum's rounding: running sums reach the total before its end, and
+    pass it where they are added in another order."""
+    rng = np.random.default_rng(15)
+    n = 40
+    b = Batch([1] * n, 2, seed=15, certain=certain)
+    logits = rng.standard_normal((b.rows, vocab)) * 3.0
+    logits[:, vocab // 2:] -= 50.0
+    b.p, b.vocab = _softmax(logits), vocab
+    b.q = None if certain else _softmax(logits + 0.4 * rng.standard_normal(logits.shape))
+    b.tokens = np.zeros(b.rows, np.int64)
+    b.u[:] = 1.0  # (half of the first rows are refused where drafts are not certain)
+    for w in (1.0, 1.5, np.inf, np.nan):
+        b.w[:] = w
+        got = [x.cpu().numpy() for x in nv.nvfp4_verify_drafted(**b.device())]
+        for r in range(n):
+            row = 2 * r + got[0][r]
+            left = b.p[row].astype(np.float64)
+            if got[0][r] == 0 and certain:
+                left[0] = 0.0
+            elif got[0][r] == 0:
+                left = left - b.q[row]
+            assert got[1][row] == np.flatnonzero(left > 0)[-1], (w, r)
