@@ -315,7 +315,8 @@ nvfp4_status nvfp4_verify_drafted(const float* target_probs, int64_t target_ld, 
                                   const int32_t* query_start, int64_t requests, const float* accept_u,
                                   const float* sample_u, int32_t* accepted, int32_t* out_tokens,
                                   void* workspace, int64_t workspace_bytes, void* stream) {
-  if (rows < 0 || rows > kMaxI32 || vocab < 1 || vocab > kMaxI32 - nvfp4::kVerifyChunk || requests < 0 ||
+  // (the kernels' steps over rows and tokens stay below 2^31 too)
+  if (rows < 0 || rows > kMaxI32 - nvfp4::kVerifyChunk || vocab < 1 || vocab > kMaxI32 - nvfp4::kVerifyChunk || requests < 0 ||
       requests > NVFP4_MAX_REQUESTS || target_ld < vocab || (draft_probs && draft_ld < vocab))
     return NVFP4_ESHAPE;
   if (rows > 0 && (target_ld > kMaxSpan / rows || (draft_probs && draft_ld > kMaxSpan / rows))) return NVFP4_ESHAPE;

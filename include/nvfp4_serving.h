@@ -204,7 +204,7 @@ int64_t nvfp4_kv_fp4_attention_workspace(int64_t tokens, int64_t heads, int64_t 
  *
  *   target_probs  device, float [rows, vocab], row pitch target_ld >= vocab (elements); 4-byte aligned.
  *   draft_probs   device, float [rows, vocab], row pitch draft_ld, or NULL; its row s + n is not read.
- *   rows, vocab   rows >= 0, 1 <= vocab < 2^31 - 4096; rows * ld <= 2^40.
+ *   rows, vocab   0 <= rows < 2^31 - 4096, 1 <= vocab < 2^31 - 4096; rows * ld <= 2^40.
  *   tokens        device, int32[rows]: the step's input tokens.
  *   query_start   device, int32[requests + 1]; entries are clamped to [0, rows].
  *   accept_u      device, float[rows] (entry s + n is not read); sample_u: device, float[requests]; both of [0, 1).

@@ -214,6 +214,13 @@ def test_verify_validation():
     assert 0 < ws(8192, 2 ** 31 - 5000) < 2 ** 37
 
 
+def test_rows_whose_numbers_leave_32_bits_are_refused():
+    """A workgroup steps over a request's rows by 64 and 256: past a last row close to 2^31 the step would overflow."""
+    for rows in (2 ** 31 - 1, 2 ** 31 - 256, 2 ** 31 - 4096):
+        assert _verify(rows=rows, V=1, pld=1, qld=1) == ESHAPE, rows
+    assert _verify(rows=2 ** 31 - 4097, V=1, pld=1, qld=1, ws=None) == EINVAL
+
+
 # ---- the binding ------------------------------------------------------------------------------
 
 
