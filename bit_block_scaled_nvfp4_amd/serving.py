@@ -296,6 +296,8 @@ def nvfp4_kv_fp8_append(key, value, positions, inv_freq, key_scale, value_scale,
     if value_cache.shape[0] != slots or (slots > 1 and value_cache.stride(0) != strides[0]):
         raise ValueError("value_cache must have key_cache's slots and row pitch")
     ld = strides[0] if slots > 1 else max(width, shape[1] // 16 * 16)
+    if ld < width:
+        raise ValueError(f"caches must have rows of their own (row pitch {ld}, {width} a row): no expanded or overlapping views")
     kp, vp = key_cache.data_ptr(), value_cache.data_ptr()
     extent = (slots - 1) * ld + width if slots else 0
     if kp < vp + extent and vp < kp + extent and not width <= (vp - kp) % ld <= ld - width:

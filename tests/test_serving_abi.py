@@ -326,6 +326,17 @@ def test_binding_checks_of_the_appends():
                 fn(**a)
 
 
+def test_caches_whose_rows_share_memory_are_refused():
+    import torch
+
+    bf, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
+    row = _t((1, 256), u8)
+    for kc, vc in ((row.expand(32, 256), row.expand(32, 256)), (_t((1, 256), u8).expand(32, 256), row.expand(32, 256)),
+                   (_t((8192,), u8).as_strided((32, 256), (128, 1)), _t((8192,), u8).as_strided((32, 256), (128, 1)))):
+        with pytest.raises(ValueError, match="rows of their own"):
+            nv.nvfp4_kv_fp8_append(_Dev(_t((6, 2, 128), bf)), _t((6, 2, 128), bf), None, None, _t((1,), f32), _t((1,), f32), kc, vc)
+
+
 def test_ranges_that_meet_are_refused():
     sv._refuse_ranges([("a", 0, 16), ("b", 16, 32)], [("x", 32, 64), ("y", 40, 50), ("z", 7, 7)])
     for outs, ins in (([("a", 0, 16), ("b", 15, 32)], []), ([("a", 10, 20)], [("x", 0, 11)]), ([("a", 10, 20)], [("x", 0, 100)])):
