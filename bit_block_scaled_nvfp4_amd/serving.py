@@ -341,7 +341,8 @@ def nvfp4_kv_fp4_append(key, value, positions, inv_freq, key_gscale, value_gscal
                         interleaved=False):
     """Norm and rotate the new tokens' keys and write keys and values into the 4-bit cache, each head's row encoded as
     NVFP4 under the static scale ``key_gscale`` or ``value_gscale`` (the block scale's factor is ``g * fl(1/6)``, not the
-    ``g / 6`` of :func:`nvfp4_quantize`, a neighbour at most: maxima in the middle between two scales may take the other).
+    ``g / 6`` of :func:`nvfp4_quantize`, a neighbour at most: maxima in the middle between two scales may take the other; the same
+    where ``g`` is six times a float32 number).
 
     Codes: uint8 ``[num_blocks, kv_heads, block_size, head_dim / 2]``, scales: uint8 ``[..., head_dim / 16]``, contiguous.
     ``slot_mapping`` (int64 ``[tokens]``; None: token t in slot t) counts ``block * block_size + place``, as

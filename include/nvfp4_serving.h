@@ -17,7 +17,8 @@
  * V(code) * E4M3(scale) / g.  One step differs: the block scale's factor is the product fl(g * fl(1/6)), not the
  * quotient fl(g / 6) of nvfp4_quantize.  The two are equal or neighbours, so a block takes another scale than there
  * only where its scaled maximum lies within 2^-22 of the middle between two scale codes, where either is as near.
- * Slot s of a slot map is row s % block_size of block
+ * Where g is six times a binary32 number the factors are the same number, and so are all codes and scales.  Slot s of a
+ * slot map is row s % block_size of block
  * s / block_size, as in the FP8 cache, so nvfp4_kv_block_tables serves both.  A KV head's rows of a block
  * lie together: 9/16 byte an element, read in whole lines.
  *

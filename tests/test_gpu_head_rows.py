@@ -14,6 +14,7 @@ import oracle
 from oracle import serving as osv
 
 from .attention_util import to_type
+from .fp4_scale_util import middle_maxima, scale_code
 from .gpu_util import DEV, log
 
 pytestmark = pytest.mark.gpu
@@ -434,3 +435,31 @@ def test_numbers_of_other_types_are_taken():
     want = nv.nvfp4_qk_norm_rope(q, k, **d, eps=0.125, weight_offset=0.5, interleaved=True)
     got = nv.nvfp4_qk_norm_rope(q, k, **d, eps=np.float32(0.125), weight_offset=np.float64(0.5), interleaved=np.True_)
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("g", [56.0, 448.0, 200.0, 140.0, 300.0, 3.0])
+def test_fp4_scales_at_the_middles_between_codes(g, dtype):
+    """The scale by its definition where the choice between two codes turns; and, where the encoder's factor g / 6 is the
+    same number as the cache's g fl(1/6) (140, 300, 3), the tensor encoder's codes and scales to the last bit."""
+    import torch
+
+    maxima = np.unique(_values(middle_maxima(g), dtype))
+    rng = np.random.default_rng(16)
+    rows = -(-len(maxima) // 4)
+    x = rng.uniform(-1.0, 1.0, (rows * 4, 16)).astype(np.float32)
+    peak = np.resize(maxima, rows * 4).astype(np.float32)
+    x = _values(x * peak[:, None], dtype)
+    x[np.arange(rows * 4), rng.integers(0, 16, rows * 4)] = peak * rng.choice([-1.0, 1.0], rows * 4).astype(np.float32)
+    x = x.reshape(rows, 1, 64)
+    log(f"middles g={g} {dtype}")
+    gs = torch.tensor([g], device=DEV)
+    cache = _cache4(1, 1, rows, 64)
+    nv.nvfp4_kv_fp4_append(_up(x, dtype), _up(-x, dtype), None, None, gs, gs, *cache)
+    codes, scales, back, same_scales = (_rows4(t, np.arange(rows)) for t in cache)
+    want = np.array([scale_code(a, g) for a in np.abs(x).reshape(-1, 16).max(1)]).reshape(rows, 1, 4)
+    assert np.array_equal(scales, want) and np.array_equal(same_scales, want)
+    assert np.array_equal(codes, osv.encode4(x, g)[0]) and np.array_equal(back, osv.encode4(-x, g)[0])
+    if np.float32(g) / np.float32(6) == np.float32(g) * (np.float32(1) / np.float32(6)):
+        qc, qs, _ = nv.nvfp4_quantize(_up(x.reshape(rows, 64), dtype), gs)
+        assert np.array_equal(qc.cpu().numpy().reshape(codes.shape), codes) and np.array_equal(qs.cpu().numpy().reshape(scales.shape), scales)

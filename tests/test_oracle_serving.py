@@ -11,6 +11,8 @@ import oracle
 from oracle import attention as oa
 from oracle import serving as osv
 
+from .fp4_scale_util import SIXTH, middle_maxima, scale_code
+
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 def test_rounding_is_the_types_own(dtype):
@@ -82,6 +84,42 @@ def test_rows_of_the_cache():
     back = osv.decode4(*osv.encode4(x, 3.0)) / 3.0
     assert np.abs(back - x).max() <= np.abs(x).max() / 5  # E2M1's widest step, 4 to 6, less a scale's rounding
     assert osv.decode4(np.array([[0x77] * 8], np.uint8), np.array([[0xFF]], np.uint8)).max() == 6 * 480
+
+
+@pytest.mark.parametrize("g", [56.0, 448.0, 200.0, 140.0, 300.0, 3.0])
+def test_scales_of_the_cache_at_the_middles(g):
+    """Blocks whose maximum lies next to the middle between two scale codes: the code by the definition alone, step by
+    step (fp4_scale_util)."""
+    maxima = middle_maxima(g)
+    x = np.zeros((len(maxima), 1, 16), np.float32)
+    x[:, 0, 3] = -maxima
+    got = osv.encode4(x, g)[1][:, 0, 0]
+    assert np.array_equal(got, [scale_code(a, g) for a in maxima])
+    # the tensor encoder's factor is the quotient: the same codes where it is the same number, else next to them
+    other = oracle.quantize(x[:, 0], np.float32(g))[1].reshape(-1)
+    alike = np.float32(g) / np.float32(6) == np.float32(g) * (np.float32(1) / np.float32(6))
+    assert alike == (g in (140.0, 300.0, 3.0))
+    assert np.array_equal(got, other) if alike else 0 < np.sum(got != other) and np.abs(got.astype(int) - other).max() == 1
+
+
+def test_a_global_scale_of_six_times_a_number_has_one_factor():
+    """g = 6 x, exactly: fl(g / 6) = x, and g fl(1/6) = x (1 + 2^-25), less than half a place from x."""
+    assert Fraction(SIXTH) * 6 == 1 + Fraction(1, 2 ** 25)
+    x = np.random.default_rng(6).uniform(1, 2, 100000).astype(np.float32)
+    x = x.view(np.uint32) & ~np.uint32(7)  # three bits for the product with 6
+    x = np.concatenate([x.view(np.float32), np.float32([1.0, 2.0 - 2.0 ** -20])])
+    g = x * np.float32(6)
+    assert np.array_equal(g.astype(np.float64), x.astype(np.float64) * 6)
+    assert np.array_equal(g / np.float32(6), x) and np.array_equal(g * np.float32(SIXTH), x)
+
+
+def test_scales_of_the_cache_by_hand():
+    """2.25 * 56 / 6 is 21, the middle between 20 (0x5A) and 22 (0x5B): fl(56 / 6) is below 56 / 6 and the product rounds to 21
+    itself, a tie (even: 20); fl(56 fl(1/6)) is the next number, above it, and the product 21 + 2^-19: 22."""
+    x = np.zeros((1, 1, 16), np.float32)
+    x[0, 0, 0] = 2.25
+    assert scale_code(2.25, 56.0) == 0x5B and osv.encode4(x, 56.0)[1].item() == 0x5B
+    assert oracle.quantize(x[0], np.float32(56.0))[1].item() == 0x5A
 
 
 def test_attention_takes_decoded_rows():
