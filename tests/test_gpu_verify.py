@@ -300,3 +300,13 @@ def test_numbers_of_one_and_more_take_the_last_token_with_a_weight(vocab, certai
             elif got[0][r] == 0:
                 left = left - b.q[row]
             assert got[1][row] == np.flatnonzero(left > 0)[-1], (w, r)
+
+
+def test_starts_that_fall_and_rows_without_a_weight():
+    """A request that finds no token to sample leaves a later one's rows alone too."""
+    b = Batch([0] * 4, 5000, seed=17, pad=8)
+    b.start = np.array([0, 7, 3, 10, 6])
+    b.u[:] = 1e9  # nothing is accepted
+    b.p[0] = 0.0
+    got = check(b, "an empty first row")
+    assert got[0].tolist() == [0, 0, 0, 0] and got[1][0] == -1 and got[1][3] >= 0
