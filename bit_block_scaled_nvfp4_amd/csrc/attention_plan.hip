@@ -85,14 +85,18 @@ AttnPlan plan_attention(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t
 
 AttnPlan plan_attention_fp4(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t requests,
                             int64_t max_query_len, int64_t max_seq_len) {
+  // The rules but for the 48 rows and the eight wavefronts are the FP8 cache's, with its figures.  What they give of fresh prompts was
+  // timed over this cache too, shared out (where they share) against row tiles, us in a graph: 24 heads over 4 of 256 dims, 512
+  // tokens 64 and 51, 1000 88 and 82, 2048 177 and 153; 32 over 8 of 128 dims, 300 36 and 20, 512 35 and 27, 1000 54 and 42, 2048 not shared 79
+  // (shared 84); 8 heads of 64 dims, 2048 37 and 53, 2700 50 and 66.  As over the FP8 cache, shares lose but at 64 dims.
   AttnPlan p = plan(tokens, heads, kv_heads, head_dim, requests, max_query_len, max_seq_len, stream_groups_fp4,
                     head_dim <= 128 ? 48 : 32);
   // Eight wavefronts an item where each has a compute unit of its own and some steps to share: two a SIMD fill each
   // other's waits.  Four against eight (us on the device, one token, 16 heads over 4): 500 positions of 64 and 128 dims 8.8 and
   // 7.8, 9.9 and 9.0, 1000 positions 12.9 and 10.4, 14.9 and 12.6; 64 requests 15.3 and 12.1, 16.6 and 14.7; 6 tokens, 64
-  // dims 11.2 and 10.2, 15.9 and 13.4.  Not of 200 positions (7.4 and 7.3 of 128 dims, 64 requests 8.4 and 8.3), and not where a
-  // SIMD's instructions are what takes the time: 256 dims 12.9 and 12.7, 19.5 and 18.1 (200 positions 8.9 and 9.5), 32 rows of
-  // 128 dims 12.2 and 12.1, 17.5 and 16.1 (200 positions 9.3 and 10.1).
+  // dims 11.2 and 10.2, 15.9 and 13.4.  Of 200 positions they gain nothing (7.4 and 7.3 of 128 dims, 64 requests 8.4 and 8.3).  Left out where
+  // a SIMD's instructions are most of the time, so that they gain less there and lose at 200 positions: 256 dims 12.9 and 12.7, 19.5 and 18.1
+  // (200 positions 8.9 and 9.5), 32 rows of 128 dims 12.2 and 12.1, 17.5 and 16.1 (200 positions 9.3 and 10.1).
   p.wide = p.workers == 0 && p.rows * head_dim <= 2048 && max_seq_len > 2 * kStreamUnit &&
            kv_heads * requests * p.row_tiles <= kComputeUnits;
   return p;

@@ -16,7 +16,7 @@
 // tokens of 24 and 4 heads of 256 dims with norms, a quarter rotated, 235 MB: 45 us, 5.2 TB/s; 3001 of 32 and 8 heads of
 // 128 dims in FP16, all rotated, 61 MB: 14.6 us.  16384 tokens of 4 heads of 256 dims into the 4-bit cache, 86 MB: 26 us, 17 of
 // them issue of vector instructions; 2047 of 8 heads of 128 dims into the FP8 cache, 13 MB: 7.3 us.  One
-// token: 4.1 us.
+// token: 4.2 us.
 #include "codec.h"
 #include "serving_internal.h"
 
@@ -485,10 +485,12 @@ hipError_t launch_heads(HeadArgs a, nvfp4_dtype dt, HeadSink sink, hipStream_t s
   // lanes that a token takes, of each kind
   const int64_t tasks[2] = {(int64_t)a.group[0].heads.d << lane_bits, a.group[1].src ? (int64_t)a.group[1].heads.d << lane_bits : 0};
   // Tokens of a workgroup: what gives its lanes four turns, but no more than leave every compute unit two workgroups,
-  // nor than 32 KB of cosines.  Fewer do not pay for a workgroup's start, more leave its end uneven (8192 tokens of 28
-  // heads of 256 dims, four turns at 2 tokens: 45 us at 2, 48 at 4, 51 at 8; 16384 tokens of 4 heads of 256 dims into the
-  // 4-bit cache, four turns at 8: 38 us at 2, 34 at 4, 30 at 8, 34 at 14; 2047 tokens of 8 heads of 128 dims into the FP8
-  // cache: 6.6 at 2, 6.3 at 4, 7.2 at 8, which are one workgroup a compute unit).
+  // nor than 32 KB of cosines.  Fewer do not pay for a workgroup's start, more leave its end uneven.  Measured with calls back to
+  // back in a graph, on inputs in turn (us): 8192 tokens of 28 heads of 256 dims, four turns at 2 tokens: 45 at 1, 41 at 2, 44 at 4,
+  // 47 at 8; 16384 tokens of 4 heads of 256 dims into the 4-bit cache, four turns at 8: 32 at 2, 27 at 4, 24 at 8, 25 at 14, into the
+  // FP8 cache 35, 31, 27, 31; of 8 heads of 128 dims into the FP8 cache, neighbouring pairs, four turns at 8: 16384 tokens 34, 30, 28,
+  // 33, 8192 tokens 19, 17.5, 16.6, 19; 2047 tokens, where 4 are two workgroups a compute unit, 8.8 at 1, 7.2 at 2, 7.7 at 4, 7.9 at 8:
+  // four workgroups a unit would be 6 % ahead there.
   int64_t block = 4 * kThreads / (tasks[0] + tasks[1]);
   const int64_t spread = (a.tokens + 2 * kComputeUnits - 1) / (2 * kComputeUnits);
   if (block > spread) block = spread;

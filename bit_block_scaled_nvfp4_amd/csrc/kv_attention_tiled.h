@@ -29,7 +29,8 @@
 //
 // Over the 4-bit cache staging costs more: a load for the codes and one for the scale of each piece, a product with the scale,
 // and for keys in BF16, which has no packed product, a step by way of FP32.  Chunk of 2048 over 30011, 24 heads of 256 dims over
-// 4 KV heads: 1.79 ms and 34 us for the join, 0.86 PFLOP/s together, the matrix cores busy 38 % of the time.
+// 4 KV heads: 1.75 ms and 33 us for the join under the profiler, 0.88 PFLOP/s together, the matrix cores busy 38 % of the time; a
+// call among others, not profiled, 1.70 ms, 0.92 PFLOP/s.
 #pragma once
 
 #include "kv_attention_common.h"
@@ -258,7 +259,7 @@ __device__ __forceinline__ bool stage(const Fetched4& f, const There<D>&, bool, 
   const int kk = k_key<D>(tid), c = k_chunk<D>(tid);
   // Granules 2 c and 2 c + 1 of the key: which of them first is chosen so that 16 neighbouring lanes of a store, which
   // differ in c or in the key's low bits, touch 16 different columns, and each 8 of them columns that differ modulo 8 (without
-  // the second, half of the stores' bank conflicts: 1843 us for 1793, at 64 dims 783 for 760)
+  // the second, half of the stores' bank conflicts: 1843 us for 1793, at 64 dims 783 for 760, each pair in one run)
   const int odd = (D == 256 ? c >> 2 ^ c >> 3 : D == 128 ? c >> 2 ^ kk : kk ^ kk >> 1) & 1;
   const uint32_t k0 = f.k[0], k1 = f.k[1];
 #pragma unroll
