@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads) verify_sum_kernel(VerifyArgs a) {
 __global__ void __launch_bounds__(kThreads) verify_pick_kernel(VerifyArgs a) {
   __shared__ double totals[kWaves];
   __shared__ int32_t firsts[kWaves], ends[kWaves];
-  __shared__ bool fall[kWaves];
+  __shared__ bool met[kWaves];
   constexpr int32_t kNone = 0x7FFFFFFF;
   const int32_t r = blockIdx.x;
   const Rows q = rows_of(a, r);
@@ -168,9 +168,13 @@ __global__ void __launch_bounds__(kThreads) verify_pick_kernel(VerifyArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int32_t row = q.start + a.accepted[r];
   const double u = a.sample_u[r];
-  // the lowest start of the requests behind the next one, which starts behind this one's rows (the first load of it is not
-  // waited for before the end)
-  int32_t next = r + 2 + tid, lowest = next < a.requests ? a.query_start[next] : kNone;
+  // the rows of a request behind the next one, which starts behind this one's rows (looked at before the end only)
+  int32_t next = r + 2 + tid;
+  int32_t from = 0, to = 0;
+  if (r + 2 < a.requests) {
+    from = a.query_start[min(next, a.requests)];
+    to = a.query_start[min(next + 1, a.requests)];
+  }
   const double* sums = a.sums + (int64_t)r * a.chunks * 2;
   // the row's sum, of the weights or, where they are all zero, of the target's probabilities
   double left = 0.0, whole = 0.0;
@@ -209,9 +213,12 @@ __global__ void __launch_bounds__(kThreads) verify_pick_kernel(VerifyArgs a) {
   }
   const bool at_end = chosen < 0;
   if (at_end) chosen = last;
-  while ((next += kThreads) < a.requests) lowest = min(lowest, a.query_start[next]);
+  // whether one of them has some of this request's rows
+  const auto meets = [&](int32_t x, int32_t y) { return x < y && x <= q.last && y > q.start; };
+  bool meet = meets(from, to);
+  while ((next += kThreads) < a.requests) meet |= meets(a.query_start[next], a.query_start[next + 1]);
   int32_t token = -1;
-  bool falls = false;
+  bool shared = false;
   if (chosen >= 0) {
     const int32_t v0 = chosen * kVerifyChunk + tid * kEach;
     float p[kEach], d[kEach];
@@ -242,11 +249,11 @@ __global__ void __launch_bounds__(kThreads) verify_pick_kernel(VerifyArgs a) {
     // the lowest of the lanes' first, the highest of their ends: lanes hold rising parts of the chunk
     const uint64_t found = __ballot(first != kNone), some = __ballot(end >= 0);
     const int32_t f = found ? __shfl(first, __builtin_ctzll(found)) : kNone, e = some ? __shfl(end, 63 - __builtin_clzll(some)) : -1;
-    const bool some_fall = __any(lowest <= q.last);
+    const bool wave_meets = __any(meet);
     if (lane == 0) {
       firsts[wave] = f;
       ends[wave] = e;
-      fall[wave] = some_fall;
+      met[wave] = wave_meets;
     }
     __syncthreads();
     int32_t at = kNone, tail = -1;
@@ -254,15 +261,15 @@ __global__ void __launch_bounds__(kThreads) verify_pick_kernel(VerifyArgs a) {
     for (int k = 0; k < kWaves; ++k) {
       at = min(at, firsts[k]);
       tail = max(tail, ends[k]);
-      falls |= fall[k];
+      shared |= met[k];
     }
     // (where rounding leaves the chunk's sum at the aim: its last token with a weight)
     token = at_end || at == kNone ? tail : at;
   } else {
-    falls = __syncthreads_or(lowest <= q.last);
+    shared = __syncthreads_or(meet);
   }
   for (int32_t t = q.start + tid; t <= q.last; t += kThreads) {
-    if (__builtin_expect(falls, 0) && taken_later(a, r, t)) continue;
+    if (__builtin_expect(shared, 0) && taken_later(a, r, t)) continue;
     a.out[t] = t < row ? a.tokens[t + 1] : t == row ? token : -1;
   }
 }

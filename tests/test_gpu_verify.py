@@ -310,3 +310,11 @@ def test_starts_that_fall_and_rows_without_a_weight():
     b.p[0] = 0.0
     got = check(b, "an empty first row")
     assert got[0].tolist() == [0, 0, 0, 0] and got[1][0] == -1 and got[1][3] >= 0
+
+
+def test_a_batch_padded_with_requests_at_row_zero():
+    """Starts of zero behind the last request: none of its rows, or of the others', is theirs."""
+    b = Batch([3, 0, 5, 2] + [0] * 400, 300, seed=18)
+    b.start[5:] = 0
+    got = check(b, "starts of zero behind the last request")
+    assert np.all(got[1][:14] >= -1) and np.all(got[1][14:] == -7)
