@@ -29,7 +29,7 @@
 //
 // Over the 4-bit cache staging costs more: a load for the codes and one for the scale of each piece, a product with the scale,
 // and for keys in BF16, which has no packed product, a step by way of FP32.  Chunk of 2048 over 30011, 24 heads of 256 dims over
-// 4 KV heads: 1.75 ms and 33 us for the join under the profiler, 0.88 PFLOP/s together, the matrix cores busy 38 % of the time; a
+// 4 KV heads: 1.72 ms and 33 us for the join under the profiler, 0.89 PFLOP/s together, the matrix cores busy 38 % of the time; a
 // call among others, not profiled, 1.70 ms, 0.92 PFLOP/s.
 #pragma once
 

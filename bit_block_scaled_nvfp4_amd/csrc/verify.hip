@@ -8,7 +8,7 @@
 // element and writes the tokens.  Sums are binary64 in a fixed order: weights are differences of binary32 numbers, so
 // two orders differ by about 2^-50 of the sum.
 //
-// Measured (copies at 4.9 TB/s): 64 requests of up to 8 drafts over 131077 tokens, 64 MB: 13.8 us for the sums and 5.8 for the
+// Measured (copies at 4.9 TB/s): 64 requests of up to 8 drafts over 131077 tokens, 64 MB: 13.6 us for the sums and 5.8 for the
 // tokens (10 with barriers and single loads); one request over 32000: 4.8 and 5.1, the start of a launch and the chain of
 // loads.
 #include "serving_internal.h"
